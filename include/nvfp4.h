@@ -396,6 +396,132 @@ NVFP4_API nvfp4_status_t nvfp4_gdn_recurrence(const void *q_bf16, const void *k_
                                               int out_kind, nvfp4_stream_t stream);
 
 /*
+ * The attention layer around the linears: head norms with the position rotation, a paged
+ * 8-bit KV cache with one scale per (block of tokens, head), attention over it, and
+ * products of a few tokens with a 4-bit weight.  The pages have 16 attention layers whose
+ * KV cache is FP8 (blog section "KVキャッシュはFP8で十分？") but give no formulas for them;
+ * the ones below are this library's.
+ */
+
+/* A paged K / V cache in E4M3.  Block b of kv head h holds block_size tokens of head_dim
+ * values at ((b * n_kv_heads + h) * block_size + i) * head_dim, i the token's place in the
+ * block; its values mean e4m3(code) * scales[b * n_kv_heads + h].  Owned by the caller;
+ * needs no initialisation.  block_size: 16, 32, 64 or 128; head_dim: 64, 128 or 256. */
+typedef struct {
+  uint8_t *k, *v;               /* device, 16-byte aligned */
+  float *k_scales, *v_scales;   /* device FP32 [num_blocks][n_kv_heads] */
+  int64_t num_blocks;
+  int block_size, n_kv_heads, head_dim;
+} nvfp4_block_cache_t;
+
+/* A batch of sequences with new tokens, packed one after another.  Sequence s has the token
+ * rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (none is allowed), which are the last of its
+ * kv_lens[s] tokens; its position p lives in cache block block_table[s][p / block_size].
+ * A sequence whose bounds are not 0 <= start <= end <= tokens, or with kv_lens[s] outside
+ * [0, max_blocks * block_size], is skipped, and a block outside [0, num_blocks) is never
+ * touched; both are reported as NVFP4_ERR_DEVICE_INDEX by nvfp4_get_device_status.  Token
+ * rows behind the last sequence are left as they are. */
+typedef struct {
+  const int32_t *cu_seqlens;    /* device int32 [n_seqs + 1] */
+  const int32_t *kv_lens;       /* device int32 [n_seqs] */
+  const int32_t *block_table;   /* device int32 [n_seqs x ld_table]; entries of places behind a
+                                 * sequence's end are not read */
+  int64_t n_seqs, tokens;       /* n_seqs <= 65535; tokens: rows of the q / k / v / out buffers, 0 allowed */
+  int64_t max_blocks, ld_table; /* columns, row stride */
+} nvfp4_batch_t;
+
+/*
+ * nvfp4_rope_table - table of the position rotation for nvfp4_qk_norm_rope:
+ *   table[p * rot_dim + i] = cos(a), table[p * rot_dim + rot_dim/2 + i] = sin(a),
+ *   a = p * base^(-2i / rot_dim), for p < max_pos, i < rot_dim / 2; computed in FP64, stored
+ *   in FP32.  Callers with other angles (scaled or interpolated positions) fill the table
+ *   themselves.  table: device, 16-byte aligned; rot_dim % 16 == 0, <= 256; base > 0.
+ */
+NVFP4_API nvfp4_status_t nvfp4_rope_table(float *table, int64_t max_pos, int rot_dim, double base,
+                                          nvfp4_stream_t stream);
+
+/*
+ * nvfp4_qk_norm_rope - RMS norm of each query and key head, then the position rotation, in
+ *   one pass.  For a head x of head_dim values with the weight w (w_q or w_k):
+ *     y   = x / sqrt(mean(x^2) + eps) * (w_offset + w)
+ *     for i < rot_dim / 2, (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved:
+ *     y_a' = y_a c - y_b s,  y_b' = y_b c + y_a s,   c, s = row positions[t] of the table.
+ *   FP32 arithmetic, one rounding to BF16.  Squares outside FP32's range are handled.
+ *   q, k: device BF16 rows, head h at column h * head_dim, 16-byte aligned, ld % 8 == 0
+ *   (column ranges of one projection's output are fine).  q_out, k_out: likewise; each may
+ *   be its input (same pointer and stride), otherwise no overlap.  w_q, w_k: BF16
+ *   [head_dim], 16-byte aligned.  positions: device int64 [tokens], 0 <= p < max_pos; a
+ *   token whose position is outside is left unwritten and reported as
+ *   NVFP4_ERR_DEVICE_INDEX.  rot_dim: multiple of 16, 0 (no rotation; positions and table
+ *   may be NULL) .. head_dim.  head_dim: 64, 128 or 256.  tokens == 0 does nothing.
+ */
+NVFP4_API nvfp4_status_t nvfp4_qk_norm_rope(const void *q_bf16, int64_t ld_q, const void *k_bf16, int64_t ld_k,
+                                            int64_t tokens, int n_heads, int n_kv_heads, int head_dim,
+                                            const void *w_q_bf16, const void *w_k_bf16, float w_offset, float eps,
+                                            const int64_t *positions, const float *table, int64_t max_pos,
+                                            int rot_dim, int interleaved, void *q_out, int64_t ld_qo, void *k_out,
+                                            int64_t ld_ko, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_kv_append - quantise the new tokens' K and V rows into the cache.  For every block
+ *   that gets new tokens, each kv head, K and V apart:
+ *     s = the smallest power of two, at least 2^-100, with 448 s >= max|x| over the new
+ *         values; if the block holds earlier tokens, at least its present scale;
+ *     new codes = E4M3(x / s);  earlier codes, if s grew: E4M3(code * (old scale / s)),
+ *   nearest even.  A power of two costs no precision in a floating code, and an earlier code
+ *   changes only where it becomes subnormal.  Infinities become +-448 s and NaN a NaN code;
+ *   neither sets the scale.  Other places of the block are left as they are.
+ *   k, v: device BF16 [tokens x ld], kv head h at column h * head_dim, 16-byte aligned,
+ *   ld % 8 == 0.  A sequence with kv_lens[s] below its number of new tokens is skipped and
+ *   reported.  The blocks that one call writes must be distinct: a block that two sequences
+ *   share (a common prefix) must be full before either appends behind it.
+ */
+NVFP4_API nvfp4_status_t nvfp4_kv_append(const void *k_bf16, int64_t ld_k, const void *v_bf16, int64_t ld_v,
+                                         const nvfp4_batch_t *batch, const nvfp4_block_cache_t *cache,
+                                         nvfp4_stream_t stream);
+
+/* Bytes of the workspace nvfp4_attention needs for these sizes (0 for invalid ones). */
+NVFP4_API size_t nvfp4_attention_workspace_bytes(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads,
+                                                 int head_dim);
+
+/*
+ * nvfp4_attention - attention of the batch's token rows over the cache, prompts and single
+ *   tokens alike (the new tokens' K and V are in the cache already, see nvfp4_kv_append):
+ *     out[t, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(softmax_scale * q[t, h] . k_j)
+ *   over the tokens j of t's sequence, kv head h / (n_heads / n_kv_heads).  With causal != 0
+ *   the i-th of n new tokens sees j <= kv_len - n + i, otherwise all kv_len.  A row that sees
+ *   no token is 0.  What no row sees (places behind a sequence's end, later tokens) has no
+ *   influence, NaN included.  FP32 maxima, sums and accumulators; q and the weights p enter
+ *   the products as FP16, q scaled by a power of two per row so that it keeps its BF16 bits
+ *   down to 2^-29 of the row's largest value, p rounded to 11 bits.
+ *   q: device BF16 [tokens x ld_q], head h at column h * head_dim, 16-byte aligned,
+ *   ld_q % 8 == 0.  out: device, BF16 (ld_out % 8 == 0) or FP32 (ld_out % 4 == 0) per
+ *   out_kind, 16-byte aligned.  Cache scales must be positive; powers of two (as
+ *   nvfp4_kv_append writes) are exact, others are taken to within 2^-17.
+ *   workspace: device, >= nvfp4_attention_workspace_bytes(...) bytes, 16-byte aligned;
+ *   contents on entry do not matter.  Calls that share one must not overlap on the GPU.
+ *   Results do not depend on the order in which CTAs run.
+ */
+NVFP4_API nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, const nvfp4_batch_t *batch,
+                                         const nvfp4_block_cache_t *cache, float softmax_scale, int causal,
+                                         void *out, int out_kind, int64_t ld_out, void *workspace,
+                                         size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_matvec - product of 1 to 16 tokens with an NVFP4 weight, activations in BF16 (not
+ *   quantised, unlike nvfp4_linear): the single-token form of a projection.
+ *     out[m, n] = (sum_k x[m, k] e2m1(W[n, k]) e4m3(sfW[n, k / 16])) / gs_w(seg(n))
+ *   The products of codes and block scales are exact in FP16; x is scaled by a power of two
+ *   per 1024 columns and keeps its BF16 bits down to 2^-29 of their largest; FP32 sums.
+ *   x: device BF16 [M x ld_x], 16-byte aligned, ld_x % 8 == 0.  W: as in nvfp4_linear, with
+ *   K % 64 == 0, codes 32-byte aligned, any number of rows.  segs: as in nvfp4_linear, with
+ *   no alignment of their bounds.  out: BF16 or FP32 per out_kind, ldo >= N, any ldo.
+ */
+NVFP4_API nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const nvfp4_operand_t *W,
+                                      const nvfp4_segment_t *segs, int nseg, void *out, int out_kind, int64_t ldo,
+                                      nvfp4_stream_t stream);
+
+/*
  * nvfp4_get_device_status - read and clear the device status word of the current
  * device.  Kernels never spin forever: every wait on an mbarrier has an iteration
  * limit, and a wait that runs out records NVFP4_ERR_DEVICE_TIMEOUT here and the

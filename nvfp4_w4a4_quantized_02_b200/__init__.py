@@ -17,6 +17,8 @@ __all__ = [
     "linear_splitk", "linear_splitk_noalloc", "noalloc_default_splits", "splitk_default", "splitk_workspace_bytes",
     "NOALLOC_SCRATCH_BYTES", "fold_segments", "fp8_scale", "kv_cache_fp8", "gdn_recurrence",
     "device_status", "selftest_stalled_linear", "unswizzle_scales", "pack_weight", "NVFP4Tensor", "EPILOGUES", "OUT_KINDS",
+    "BlockKVCache", "block_kv_cache", "rope_table", "qk_norm_rope", "kv_append", "attention",
+    "attention_workspace_bytes", "matvec",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +50,16 @@ class EpilogueParams(ctypes.Structure):
                 ("gs_out", _c_vp), ("out_scales", _c_vp)]
 
 
+class BlockCache(ctypes.Structure):
+    _fields_ = [("k", _c_vp), ("v", _c_vp), ("k_scales", _c_vp), ("v_scales", _c_vp), ("num_blocks", _c_i64),
+                ("block_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class Batch(ctypes.Structure):
+    _fields_ = [("cu_seqlens", _c_vp), ("kv_lens", _c_vp), ("block_table", _c_vp), ("n_seqs", _c_i64),
+                ("tokens", _c_i64), ("max_blocks", _c_i64), ("ld_table", _c_i64)]
+
+
 class NVFP4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -59,7 +71,9 @@ SYMBOLS = ("nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_global_scale", "nv
            "nvfp4_quantize_rows", "nvfp4_linear", "nvfp4_linear_splitk", "nvfp4_splitk_workspace_bytes",
            "nvfp4_splitk_default", "nvfp4_linear_splitk_noalloc", "nvfp4_fold_segments",
            "nvfp4_fp8_scale", "nvfp4_kv_cache_fp8", "nvfp4_gdn_recurrence", "nvfp4_get_device_status",
-           "nvfp4_selftest_stalled_linear", "nvfp4_unswizzle_scales", "nvfp4_pack_weight", "nvfp4_amax")
+           "nvfp4_selftest_stalled_linear", "nvfp4_unswizzle_scales", "nvfp4_pack_weight", "nvfp4_amax",
+           "nvfp4_rope_table", "nvfp4_qk_norm_rope", "nvfp4_kv_append", "nvfp4_attention_workspace_bytes",
+           "nvfp4_attention", "nvfp4_matvec")
 
 
 def lib():
@@ -123,6 +137,23 @@ def lib():
     L.nvfp4_selftest_stalled_linear.argtypes = [ctypes.POINTER(Operand), _c_vp, ctypes.POINTER(Operand),
                                                 ctypes.POINTER(Segment), ctypes.c_int, _c_vp, _c_i64, ctypes.c_int,
                                                 _c_vp]
+    c_int, c_float = ctypes.c_int, ctypes.c_float
+    L.nvfp4_rope_table.restype = c_int
+    L.nvfp4_rope_table.argtypes = [_c_vp, _c_i64, c_int, ctypes.c_double, _c_vp]
+    L.nvfp4_qk_norm_rope.restype = c_int
+    L.nvfp4_qk_norm_rope.argtypes = [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, c_int, c_int, c_int, _c_vp, _c_vp, c_float,
+                                     c_float, _c_vp, _c_vp, _c_i64, c_int, c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp]
+    L.nvfp4_kv_append.restype = c_int
+    L.nvfp4_kv_append.argtypes = [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.POINTER(Batch), ctypes.POINTER(BlockCache),
+                                  _c_vp]
+    L.nvfp4_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.nvfp4_attention_workspace_bytes.argtypes = [_c_i64, _c_i64, c_int, c_int, c_int]
+    L.nvfp4_attention.restype = c_int
+    L.nvfp4_attention.argtypes = [_c_vp, _c_i64, c_int, ctypes.POINTER(Batch), ctypes.POINTER(BlockCache), c_float,
+                                  c_int, _c_vp, c_int, _c_i64, _c_vp, ctypes.c_size_t, _c_vp]
+    L.nvfp4_matvec.restype = c_int
+    L.nvfp4_matvec.argtypes = [_c_vp, _c_i64, _c_i64, ctypes.POINTER(Operand), ctypes.POINTER(Segment), c_int, _c_vp,
+                               c_int, _c_i64, _c_vp]
     _LIB = L
     return L
 
@@ -442,6 +473,238 @@ def gdn_recurrence(q, k, v, g, beta, cu_seqlens, state, *, initial_state=True, o
                                       _c_vp(cu_seqlens.data_ptr()), n_seqs, tokens, hk, hv, 128,
                                       _c_vp(state.data_ptr()), int(bool(initial_state)), _c_vp(out.data_ptr()),
                                       out.stride(0), kind, _stream(stream)), "nvfp4_gdn_recurrence")
+    return out
+
+
+@dataclass
+class BlockKVCache:
+    """A paged E4M3 K / V cache with one scale per (block of tokens, kv head)."""
+    k: "torch.Tensor"         # uint8 [num_blocks, n_kv_heads, block_size, head_dim]
+    v: "torch.Tensor"
+    k_scales: "torch.Tensor"  # float32 [num_blocks, n_kv_heads]
+    v_scales: "torch.Tensor"
+
+
+def block_kv_cache(num_blocks: int, n_kv_heads: int, block_size: int, head_dim: int, device="cuda") -> BlockKVCache:
+    """An empty cache (uninitialised memory; ``kv_append`` needs no more)."""
+    import torch
+    shape = (num_blocks, n_kv_heads, block_size, head_dim)
+    k, v = (torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2))
+    ks, vs = (torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+    return BlockKVCache(k, v, ks, vs)
+
+
+def _require(ok, message: str):
+    if not ok:
+        raise ValueError(message)
+
+
+def _rows(x, name: str, dtype, device=None):
+    """Checks a matrix argument (CUDA, 2-D, unit column stride) and returns its row stride."""
+    _require(x.is_cuda and x.dtype == dtype and x.dim() == 2, f"{name} must be a 2-D {dtype} CUDA tensor")
+    _require(x.shape[1] <= 1 or x.stride(1) == 1, f"{name} must have unit column stride")
+    _require(device is None or x.device == device, f"{name} is on another device")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+class _Call:
+    """Device and stream of one call: switches to the tensors' device when it is not the
+    current one, and tells the allocator about buffers allocated here that a stream other
+    than the current one uses."""
+
+    def __init__(self, device, stream, *allocated):
+        import torch
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        current = torch.cuda.current_stream(device)
+        if stream is not None and stream.cuda_stream != current.cuda_stream:
+            _require(stream.device == device, "stream is on another device")
+            for t in allocated:
+                t.record_stream(stream)
+            current = stream
+        self.stream = current.cuda_stream
+
+    def __call__(self, what, fn, *args):
+        if self.guard is not None:
+            with self.guard:
+                status = fn(*args, self.stream)
+        else:
+            status = fn(*args, self.stream)
+        if status != 0:
+            raise NVFP4Error(status, what)
+
+
+def _out_kind(out_dtype: str):
+    import torch
+    _require(out_dtype in ("bf16", "f32"), f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    return (torch.bfloat16, 0) if out_dtype == "bf16" else (torch.float32, 1)
+
+
+def _cache_struct(cache: BlockKVCache, device) -> BlockCache:
+    import torch
+    k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
+    _require(k.dim() == 4 and k.dtype == v.dtype == torch.uint8 and k.shape == v.shape, "cache k / v must be uint8 "
+             "[num_blocks, n_kv_heads, block_size, head_dim]")
+    nb, hk, block, d = k.shape
+    _require(ks.dtype == vs.dtype == torch.float32 and ks.shape == vs.shape == (nb, hk),
+             "cache scales must be float32 [num_blocks, n_kv_heads]")
+    _require(k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous(),
+             "cache tensors must be contiguous")
+    _require(k.device == v.device == ks.device == vs.device == device, "cache is on another device")
+    return BlockCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), nb, block, hk, d)
+
+
+def _batch_struct(cu_seqlens, kv_lens, block_table, tokens, device) -> Batch:
+    import torch
+    i32 = torch.int32
+    _require(cu_seqlens.dtype == kv_lens.dtype == block_table.dtype == i32,
+             "cu_seqlens, kv_lens and block_table must be int32")
+    _require(kv_lens.dim() == 1 and cu_seqlens.shape == (kv_lens.shape[0] + 1,) and block_table.dim() == 2
+             and block_table.shape[0] == kv_lens.shape[0], "cu_seqlens [n_seqs + 1], kv_lens [n_seqs] and block_table "
+             "[n_seqs, max_blocks] disagree")
+    _require(cu_seqlens.device == kv_lens.device == block_table.device == device, "batch tensors are on another device")
+    _require(cu_seqlens.is_contiguous() and kv_lens.is_contiguous(), "cu_seqlens and kv_lens must be contiguous")
+    ld = _rows(block_table, "block_table", i32)
+    n, cols = block_table.shape
+    return Batch(cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, tokens, cols, ld)
+
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda", stream=None):
+    """FP32 [max_positions, rot_dim] table of cosines and sines for ``qk_norm_rope``, angles
+    p * base^(-2i / rot_dim) computed in FP64."""
+    import torch
+    table = torch.empty((max_positions, rot_dim), dtype=torch.float32, device=device)
+    _Call(table.device, stream, table)("nvfp4_rope_table", lib().nvfp4_rope_table, table.data_ptr(), max_positions,
+                                       rot_dim, float(base))
+    return table
+
+
+def qk_norm_rope(q, k, w_q, w_k, positions=None, table=None, *, eps: float = 1e-6, weight_offset: float = 0.0,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head and the position rotation, in one pass.
+
+    q: BF16 [tokens, heads * head_dim], k: BF16 [tokens, kv_heads * head_dim] (column ranges
+    of one projection's output allowed); w_q, w_k: BF16 [head_dim], used as
+    ``weight_offset + w``; positions: int64 [tokens]; table: FP32 [max_positions, rot_dim]
+    (``rope_table``), None for no rotation.  ``q_out`` / ``k_out`` may be ``q`` / ``k``.
+    Returns ``(q_out, k_out)``."""
+    import torch
+    bf16 = torch.bfloat16
+    ld_q = _rows(q, "q", bf16)
+    dev = q.device
+    ld_k = _rows(k, "k", bf16, dev)
+    d, tokens = w_q.numel(), q.shape[0]
+    _require(w_q.dtype == w_k.dtype == bf16 and w_q.dim() == 1 and w_q.shape == w_k.shape and d > 0
+             and w_q.is_contiguous() and w_k.is_contiguous() and w_q.device == w_k.device == dev,
+             "w_q and w_k must be BF16 [head_dim] on q's device")
+    _require(k.shape[0] == tokens and q.shape[1] % d == 0 and k.shape[1] % d == 0, "q and k must have the same rows, "
+             "of whole heads")
+    rot, most = 0, 0
+    if table is not None:
+        _require(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous() and table.device == dev,
+                 "table must be a contiguous float32 [max_positions, rot_dim] tensor on q's device")
+        most, rot = table.shape
+        _require(positions is not None and positions.dtype == torch.int64 and positions.shape == (tokens,)
+                 and positions.is_contiguous() and positions.device == dev, "positions must be int64 [tokens]")
+    made = []
+    if q_out is None:
+        q_out = torch.empty((tokens, q.shape[1]), dtype=bf16, device=dev)
+        made.append(q_out)
+    if k_out is None:
+        k_out = torch.empty((tokens, k.shape[1]), dtype=bf16, device=dev)
+        made.append(k_out)
+    ld_qo, ld_ko = _rows(q_out, "q_out", bf16, dev), _rows(k_out, "k_out", bf16, dev)
+    _require(q_out.shape == q.shape and k_out.shape == k.shape, "q_out / k_out must have the shape of q / k")
+    if tokens:
+        _Call(dev, stream, *made)("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, q.data_ptr(), ld_q, k.data_ptr(), ld_k,
+                                  tokens, q.shape[1] // d, k.shape[1] // d, d, w_q.data_ptr(), w_k.data_ptr(),
+                                  weight_offset, eps, _ptr(positions), _ptr(table), most, rot, int(interleaved),
+                                  q_out.data_ptr(), ld_qo, k_out.data_ptr(), ld_ko)
+    return q_out, k_out
+
+
+def kv_append(k, v, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, stream=None):
+    """Quantise the new tokens' K and V rows (BF16 [tokens, n_kv_heads * head_dim]) into the
+    cache.  Sequence s has the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1, the last of its
+    kv_lens[s] tokens (int32 tensors); block_table: int32 [n_seqs, max_blocks]."""
+    import torch
+    ld_k = _rows(k, "k", torch.bfloat16)
+    dev = k.device
+    ld_v = _rows(v, "v", torch.bfloat16, dev)
+    c = _cache_struct(cache, dev)
+    _require(k.shape == v.shape and k.shape[1] == c.n_kv_heads * c.head_dim, "k and v must be [tokens, n_kv_heads * "
+             "head_dim] of the cache")
+    b = _batch_struct(cu_seqlens, kv_lens, block_table, k.shape[0], dev)
+    if k.shape[0] and b.n_seqs:
+        _Call(dev, stream)("nvfp4_kv_append", lib().nvfp4_kv_append, k.data_ptr(), ld_k, v.data_ptr(), ld_v, b, c)
+
+
+def attention_workspace_bytes(tokens: int, n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().nvfp4_attention_workspace_bytes(tokens, n_seqs, n_heads, n_kv_heads, head_dim))
+
+
+def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softmax_scale: Optional[float] = None,
+              causal: bool = True, out=None, out_dtype: str = "bf16", workspace=None, stream=None):
+    """Attention of the token rows q (BF16 [tokens, heads * head_dim]) over the cache that
+    holds their K and V already (``kv_append``), prompts and single tokens alike.
+
+    softmax_scale: default head_dim ** -0.5.  workspace: a contiguous CUDA tensor of at
+    least ``attention_workspace_bytes(...)`` bytes (allocated here when None); calls that
+    share one must not overlap on the GPU.  Returns out [tokens, heads * head_dim]."""
+    import torch
+    ld_q = _rows(q, "q", torch.bfloat16)
+    dev = q.device
+    c = _cache_struct(cache, dev)
+    tokens, width = q.shape
+    _require(c.head_dim > 0 and width % c.head_dim == 0, "q must be [tokens, heads * head_dim] of the cache")
+    heads = width // c.head_dim
+    b = _batch_struct(cu_seqlens, kv_lens, block_table, tokens, dev)
+    dtype, kind = _out_kind(out_dtype)
+    made = []
+    if out is None:
+        out = torch.empty((tokens, width), dtype=dtype, device=dev)
+        made.append(out)
+    ld_out = _rows(out, "out", dtype, dev)
+    _require(out.shape == q.shape, "out must have the shape of q")
+    if tokens == 0 or b.n_seqs == 0:
+        return out
+    L = lib()
+    if workspace is None:
+        need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, heads, c.n_kv_heads, c.head_dim)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _require(workspace.is_contiguous() and workspace.device == dev, "workspace must be contiguous, on q's device")
+    scale = c.head_dim ** -0.5 if softmax_scale is None else softmax_scale
+    _Call(dev, stream, *made)("nvfp4_attention", L.nvfp4_attention, q.data_ptr(), ld_q, heads, b, c, scale, int(causal),
+                              out.data_ptr(), kind, ld_out, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size())
+    return out
+
+
+def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: str = "bf16", out=None, stream=None):
+    """x @ W^T for 1 to 16 token rows x (BF16 [tokens, K], not quantised) and an NVFP4
+    weight.  segments: list of ``(n_begin, n_end, gs_w)``; default one with ``w.gs``.
+    Returns out [tokens, N] (BF16 or FP32)."""
+    import torch
+    ld_x = _rows(x, "x", torch.bfloat16)
+    dev = x.device
+    _require(x.shape[1] == w.cols, "x must have the weight's columns")
+    _require(w.codes.device == w.scales.device == dev, "the weight is on another device")
+    dtype, kind = _out_kind(out_dtype)
+    made = []
+    if out is None:
+        out = torch.empty((x.shape[0], w.rows), dtype=dtype, device=dev)
+        made.append(out)
+    ldo = _rows(out, "out", dtype, dev)
+    _require(out.shape == (x.shape[0], w.rows), "out must be [tokens, N]")
+    if segments is None:
+        segments = ((0, w.rows, w.gs),)
+    _require(len(segments) <= MAX_SEGMENTS, "too many segments")
+    segs = (Segment * len(segments))(*[Segment(int(n0), int(n1), _ptr(g)) for n0, n1, g in segments])
+    _Call(dev, stream, *made)("nvfp4_matvec", lib().nvfp4_matvec, x.data_ptr(), ld_x, x.shape[0],
+                              Operand(w.codes.data_ptr(), w.scales.data_ptr(), w.rows, w.cols), segs, len(segments),
+                              out.data_ptr(), kind, ldo)
     return out
 
 

@@ -6,6 +6,8 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -19,6 +21,10 @@
 #include "gdn.cuh"
 #include "gdn_chunk.cuh"
 #include "layout.cuh"
+#include "attn_decode.cuh"
+#include "headnorm.cuh"
+#include "kvblock.cuh"
+#include "matvec.cuh"
 
 using namespace nvfp4;
 
@@ -33,6 +39,7 @@ struct DeviceInfo {
   bool attrs = false;
   int quant_ctas_per_sm = 1;
   int gemm2_clusters = 1;  // co-resident 2-CTA clusters of gemm2_kernel
+  int attn_ctas_per_sm[3] = {1, 1, 1};  // of attn::decode_kernel at head size 64, 128, 256
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -99,6 +106,13 @@ nvfp4_status_t current_device(DeviceInfo **info) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, quantize_kernel, kQThreads, kQSmemBytes) != cudaSuccess)
       return NVFP4_ERR_CUDA;
     d.quant_ctas_per_sm = occ < 1 ? 1 : occ;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.attn_ctas_per_sm[0], attn::decode_kernel<64>, attn::kThreads,
+                                                      0) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.attn_ctas_per_sm[1], attn::decode_kernel<128>, attn::kThreads,
+                                                      0) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.attn_ctas_per_sm[2], attn::decode_kernel<256>, attn::kThreads,
+                                                      0) != cudaSuccess)
+      return NVFP4_ERR_CUDA;
     d.attrs = true;
   }
   *info = &d;
@@ -269,6 +283,48 @@ nvfp4_status_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+
+// Argument checks shared by the entry points that work on a block-scaled cache.
+nvfp4_status_t check_batch(const nvfp4_batch_t *b, const nvfp4_block_cache_t *c, int *log_block) {
+  if (!b || !c || !b->cu_seqlens || !b->kv_lens || !b->block_table || !c->k || !c->v || !c->k_scales || !c->v_scales)
+    return NVFP4_ERR_INVALID_ARG;
+  if (b->n_seqs < 1 || b->tokens < 0 || b->max_blocks < 1 || b->ld_table < b->max_blocks || c->num_blocks < 1 ||
+      c->n_kv_heads < 1)
+    return NVFP4_ERR_INVALID_ARG;
+  switch (c->block_size) {
+    case 16: *log_block = 4; break;
+    case 32: *log_block = 5; break;
+    case 64: *log_block = 6; break;
+    case 128: *log_block = 7; break;
+    default: return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (b->n_seqs > 65535 || b->tokens > kMaxDim || c->n_kv_heads > 65535 || c->num_blocks > kMaxDim ||
+      b->max_blocks > (kMaxDim >> *log_block) - 1)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(b->cu_seqlens, 4) || !aligned(b->kv_lens, 4) || !aligned(b->block_table, 4) || !aligned(c->k, 16) ||
+      !aligned(c->v, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+// Workspace of nvfp4_attention: unit count, unit descriptors, partial results.
+constexpr int kMaxAttnCtas = 640;
+struct AttnWorkspace {
+  int64_t units;
+  size_t desc, desc2, part_ml, part, bytes;
+};
+AttnWorkspace attn_workspace(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim) {
+  AttnWorkspace w;
+  const int64_t group = n_heads / n_kv_heads;
+  w.units = n_kv_heads * ((tokens * group + attn::kRows - 1) / attn::kRows + n_seqs);
+  w.desc = 256;
+  w.desc2 = w.desc + w.units * sizeof(int4);
+  w.part_ml = (w.desc2 + w.units * sizeof(int2) + 255) / 256 * 256;
+  w.part = w.part_ml + size_t(2) * kMaxAttnCtas * attn::kRows * sizeof(float2);
+  w.bytes = w.part + size_t(2) * kMaxAttnCtas * attn::kRows * head_dim * sizeof(float);
+  return w;
+}
 
 // Validates the arguments of a linear and fills everything of Params but the tiling.
 nvfp4_status_t prepare_linear(const nvfp4_operand_t *A, const float *gs_a, const nvfp4_operand_t *W,
@@ -868,6 +924,241 @@ nvfp4_status_t nvfp4_gdn_recurrence(const void *q_bf16, const void *k_bf16, int6
   // About one token per sequence (decode): one warp per four state columns.
   return launch_pdl(gdn::column_kernel, dim3(gdn::kColBlocksPerHead, n_value_heads, static_cast<unsigned>(n_seqs)),
                     dim3(gdn::kColThreads), 0, s, 1, a);
+}
+
+nvfp4_status_t nvfp4_rope_table(float *table, int64_t max_pos, int rot_dim, double base, nvfp4_stream_t stream) {
+  NvtxRange nvtx("nvfp4_rope_table");
+  if (!table || max_pos < 1 || rot_dim < 1 || !(base > 0.0) || !std::isfinite(base)) return NVFP4_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0 || rot_dim > 256 || max_pos > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(table, 16)) return NVFP4_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  if (nvfp4_status_t st = current_device(&dev)) return st;
+  const int64_t want = (max_pos * (rot_dim / 2) + headnorm::kTableThreads - 1) / headnorm::kTableThreads;
+  const int64_t cap = int64_t(dev->sms) * 16;
+  return launch_pdl(headnorm::rope_table_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)),
+                    dim3(headnorm::kTableThreads), 0, reinterpret_cast<cudaStream_t>(stream), 1, table, max_pos,
+                    rot_dim, base);
+}
+
+nvfp4_status_t nvfp4_qk_norm_rope(const void *q_bf16, int64_t ld_q, const void *k_bf16, int64_t ld_k, int64_t tokens,
+                                  int n_heads, int n_kv_heads, int head_dim, const void *w_q_bf16,
+                                  const void *w_k_bf16, float w_offset, float eps, const int64_t *positions,
+                                  const float *table, int64_t max_pos, int rot_dim, int interleaved, void *q_out,
+                                  int64_t ld_qo, void *k_out, int64_t ld_ko, nvfp4_stream_t stream) {
+  NvtxRange nvtx("nvfp4_qk_norm_rope");
+  if (!q_bf16 || !k_bf16 || !w_q_bf16 || !w_k_bf16 || !q_out || !k_out) return NVFP4_ERR_INVALID_ARG;
+  if (tokens < 0 || n_heads < 1 || n_kv_heads < 1 || rot_dim < 0 || !(eps >= 0.0f) || !std::isfinite(eps) ||
+      !std::isfinite(w_offset))
+    return NVFP4_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !table || max_pos < 1)) return NVFP4_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || rot_dim % 16 != 0 || rot_dim > head_dim ||
+      n_heads > 65535 || n_kv_heads > 65535 || tokens > kMaxDim)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t wq = int64_t(n_heads) * head_dim, wk = int64_t(n_kv_heads) * head_dim;
+  if (ld_q < wq || ld_qo < wq || ld_k < wk || ld_ko < wk) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(q_bf16, 16) || !aligned(k_bf16, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(w_q_bf16, 16) || !aligned(w_k_bf16, 16) || ld_q % 8 != 0 || ld_k % 8 != 0 || ld_qo % 8 != 0 ||
+      ld_ko % 8 != 0 || (rot_dim > 0 && (!aligned(positions, 8) || !aligned(table, 16))))
+    return NVFP4_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  if (nvfp4_status_t st = current_device(&dev)) return st;
+  if (tokens == 0) return NVFP4_OK;
+  headnorm::Args a;
+  a.q = static_cast<const uint16_t *>(q_bf16);
+  a.k = static_cast<const uint16_t *>(k_bf16);
+  a.ld_q = ld_q;
+  a.ld_k = ld_k;
+  a.tokens = tokens;
+  a.heads = n_heads;
+  a.kv_heads = n_kv_heads;
+  a.w_q = static_cast<const uint16_t *>(w_q_bf16);
+  a.w_k = static_cast<const uint16_t *>(w_k_bf16);
+  a.w_offset = w_offset;
+  a.eps = eps;
+  a.positions = positions;
+  a.table = table;
+  a.max_pos = rot_dim > 0 ? max_pos : 1;
+  a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.q_out = static_cast<uint16_t *>(q_out);
+  a.k_out = static_cast<uint16_t *>(k_out);
+  a.ld_qo = ld_qo;
+  a.ld_ko = ld_ko;
+  // Few tokens: a warp takes one head group, so that all SMs have work; many: whole
+  // tokens, so that the table row and weights are read once.
+  const int per_warp = 32 / (head_dim / 8);
+  const int groups = (n_heads + n_kv_heads + per_warp - 1) / per_warp;
+  const int64_t warps = int64_t(dev->sms) * 32;
+  int64_t parts = tokens >= warps ? 1 : (warps + tokens - 1) / tokens;
+  if (parts > groups) parts = groups;
+  a.per_part = static_cast<int>((groups + parts - 1) / parts);
+  a.parts = (groups + a.per_part - 1) / a.per_part;
+  const int64_t ctas = (tokens * a.parts * 32 + headnorm::kThreads - 1) / headnorm::kThreads;
+  if (ctas > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  auto kernel = head_dim == 64 ? headnorm::head_norm_kernel<64>
+                : head_dim == 128 ? headnorm::head_norm_kernel<128> : headnorm::head_norm_kernel<256>;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(headnorm::kThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), 1, a);
+}
+
+nvfp4_status_t nvfp4_kv_append(const void *k_bf16, int64_t ld_k, const void *v_bf16, int64_t ld_v,
+                               const nvfp4_batch_t *batch, const nvfp4_block_cache_t *cache, nvfp4_stream_t stream) {
+  NvtxRange nvtx("nvfp4_kv_append");
+  int log_block = 0;
+  if (!k_bf16 || !v_bf16) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status_t st = check_batch(batch, cache, &log_block)) return st;
+  const int64_t width = int64_t(cache->n_kv_heads) * cache->head_dim;
+  if (ld_k < width || ld_v < width) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(k_bf16, 16) || !aligned(v_bf16, 16) || ld_k % 8 != 0 || ld_v % 8 != 0) return NVFP4_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  if (nvfp4_status_t st = current_device(&dev)) return st;
+  if (batch->tokens == 0) return NVFP4_OK;
+  kvblock::Args a;
+  a.k = static_cast<const uint16_t *>(k_bf16);
+  a.v = static_cast<const uint16_t *>(v_bf16);
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.cu_seqlens = batch->cu_seqlens;
+  a.kv_lens = batch->kv_lens;
+  a.tokens = batch->tokens;
+  a.n_seqs = static_cast<int>(batch->n_seqs);
+  a.kv_heads = cache->n_kv_heads;
+  a.log_d = cache->head_dim == 64 ? 6 : cache->head_dim == 128 ? 7 : 8;
+  a.table = batch->block_table;
+  a.ld_table = batch->ld_table;
+  a.max_kv = batch->max_blocks << log_block;
+  a.k_cache = cache->k;
+  a.v_cache = cache->v;
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.num_blocks = cache->num_blocks;
+  a.log_block = log_block;
+  const int64_t slots = (batch->tokens >> log_block) + 2 * batch->n_seqs;
+  const dim3 grid(static_cast<unsigned>(slots), cache->n_kv_heads, 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // Threads and 16-byte pieces per thread that hold one block of one head.
+  const int pieces = cache->block_size * cache->head_dim / 8;
+  if (pieces <= 256) return launch_pdl(kvblock::append_kernel<128, 2>, grid, dim3(128), 0, s, 1, a);
+  if (pieces <= 1024) return launch_pdl(kvblock::append_kernel<256, 4>, grid, dim3(256), 0, s, 1, a);
+  return launch_pdl(kvblock::append_kernel<512, 8>, grid, dim3(512), 0, s, 1, a);
+}
+
+size_t nvfp4_attention_workspace_bytes(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim) {
+  if (tokens < 0 || n_seqs < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || head_dim < 1) return 0;
+  if (tokens > kMaxDim || n_seqs > 65535 || n_heads > 65535 || head_dim > 256) return 0;
+  return attn_workspace(tokens, n_seqs, n_heads, n_kv_heads, head_dim).bytes;
+}
+
+nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, const nvfp4_batch_t *batch,
+                               const nvfp4_block_cache_t *cache, float softmax_scale, int causal, void *out,
+                               int out_kind, int64_t ld_out, void *workspace, size_t workspace_bytes,
+                               nvfp4_stream_t stream) {
+  NvtxRange nvtx("nvfp4_attention");
+  int log_block = 0;
+  if (!q_bf16 || !out || !workspace) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status_t st = check_batch(batch, cache, &log_block)) return st;
+  if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || !std::isfinite(softmax_scale)) return NVFP4_ERR_INVALID_ARG;
+  if (out_kind != NVFP4_OUT_BF16 && out_kind != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+  if (n_heads > 65535) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t width = int64_t(n_heads) * cache->head_dim;
+  if (ld_q < width || ld_out < width) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(q_bf16, 16) || ld_q % 8 != 0 || !aligned(out, 16) || !aligned(workspace, 16) ||
+      ld_out % (out_kind == NVFP4_OUT_BF16 ? 8 : 4) != 0)
+    return NVFP4_ERR_MISALIGNED;
+  const AttnWorkspace w = attn_workspace(batch->tokens, batch->n_seqs, n_heads, cache->n_kv_heads, cache->head_dim);
+  if (workspace_bytes < w.bytes) return NVFP4_ERR_INVALID_ARG;
+  DeviceInfo *dev = nullptr;
+  if (nvfp4_status_t st = current_device(&dev)) return st;
+  if (batch->tokens == 0) return NVFP4_OK;
+  attn::Args a;
+  a.q = static_cast<const uint16_t *>(q_bf16);
+  a.ld_q = ld_q;
+  a.cu_seqlens = batch->cu_seqlens;
+  a.kv_lens = batch->kv_lens;
+  a.tokens = batch->tokens;
+  a.n_seqs = static_cast<int>(batch->n_seqs);
+  a.kv_heads = cache->n_kv_heads;
+  a.group = n_heads / cache->n_kv_heads;
+  a.table = batch->block_table;
+  a.ld_table = batch->ld_table;
+  a.max_kv = batch->max_blocks << log_block;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.num_blocks = cache->num_blocks;
+  a.log_block = log_block;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.causal = causal != 0;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.out_fp32 = out_kind == NVFP4_OUT_F32;
+  char *base = static_cast<char *>(workspace);
+  a.n_units = reinterpret_cast<int *>(base);
+  a.desc = reinterpret_cast<int4 *>(base + w.desc);
+  a.desc2 = reinterpret_cast<int2 *>(base + w.desc2);
+  a.part_ml = reinterpret_cast<float2 *>(base + w.part_ml);
+  a.part = reinterpret_cast<float *>(base + w.part);
+  a.max_decode_rows = INT_MAX;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int i = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
+  int ctas = dev->sms * dev->attn_ctas_per_sm[i];
+  if (ctas > kMaxAttnCtas) ctas = kMaxAttnCtas;
+  auto kernel = i == 0 ? attn::decode_kernel<64> : i == 1 ? attn::decode_kernel<128> : attn::decode_kernel<256>;
+  auto combine = i == 0 ? attn::combine_kernel<64> : i == 1 ? attn::combine_kernel<128> : attn::combine_kernel<256>;
+  if (nvfp4_status_t e = launch_pdl(kernel, dim3(ctas), dim3(attn::kThreads), 0, s, 1, a)) return e;
+  return launch_pdl(combine, dim3(static_cast<unsigned>(w.units), attn::kRows), dim3(cache->head_dim / 2), 0, s, 1, a);
+}
+
+nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const nvfp4_operand_t *W,
+                            const nvfp4_segment_t *segs, int nseg, void *out, int out_kind, int64_t ldo,
+                            nvfp4_stream_t stream) {
+  NvtxRange nvtx("nvfp4_matvec");
+  if (!x_bf16 || !W || !segs || !out || !W->codes || !W->scales) return NVFP4_ERR_INVALID_ARG;
+  if (M < 1 || W->rows < 1 || W->K < 1) return NVFP4_ERR_INVALID_ARG;
+  if (out_kind != NVFP4_OUT_BF16 && out_kind != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+  if (nseg < 1 || nseg > NVFP4_MAX_SEGMENTS) return NVFP4_ERR_INVALID_ARG;
+  const int64_t N = W->rows, K = W->K;
+  if (M > 16 || N > kMaxDim || K > kMaxDim || K % 64 != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (ld_x < K || ldo < N) return NVFP4_ERR_INVALID_ARG;
+  matvec::Args a;
+  int64_t expect = 0;
+  for (int i = 0; i < nseg; ++i) {
+    if (!segs[i].gs_w || !aligned(segs[i].gs_w, 4)) return NVFP4_ERR_INVALID_ARG;
+    if (segs[i].n_begin != expect || segs[i].n_end <= segs[i].n_begin) return NVFP4_ERR_INVALID_ARG;
+    a.seg[i].n_begin = static_cast<int>(segs[i].n_begin);
+    a.seg[i].n_end = static_cast<int>(segs[i].n_end);
+    a.seg[i].gs_w = segs[i].gs_w;
+    expect = segs[i].n_end;
+  }
+  if (expect != N) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(x_bf16, 16) || ld_x % 8 != 0 || !aligned(W->codes, 32) || !aligned(W->scales, 16) ||
+      !aligned(out, out_kind == NVFP4_OUT_BF16 ? 2 : 4))
+    return NVFP4_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  if (nvfp4_status_t st = current_device(&dev)) return st;
+  a.x = static_cast<const uint16_t *>(x_bf16);
+  a.ld_x = ld_x;
+  a.M = static_cast<int>(M);
+  a.codes = W->codes;
+  a.scales = W->scales;
+  a.N = N;
+  a.K = K;
+  a.nseg = nseg;
+  a.out = out;
+  a.ldo = ldo;
+  a.out_fp32 = out_kind == NVFP4_OUT_F32;
+  const int64_t blocks = (N + matvec::kBN - 1) / matvec::kBN;
+  const int64_t chunks = (K + matvec::kChunk - 1) / matvec::kChunk;
+  int cluster = 1;
+  while (cluster < 8 && cluster * 2 <= chunks && blocks * cluster < 2 * dev->sms) cluster *= 2;
+  a.k_per_cta = (chunks + cluster - 1) / cluster * matvec::kChunk;
+  if (blocks * cluster > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid(static_cast<unsigned>(blocks * cluster));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M <= 8)
+    return launch_pdl(matvec::matvec_kernel<1>, grid, dim3(matvec::kThreads), sizeof(matvec::Smem<1>), s, cluster, a);
+  return launch_pdl(matvec::matvec_kernel<2>, grid, dim3(matvec::kThreads), sizeof(matvec::Smem<2>), s, cluster, a);
 }
 
 nvfp4_status_t nvfp4_selftest_stalled_linear(const nvfp4_operand_t *A, const float *gs_a, const nvfp4_operand_t *W,
