@@ -494,79 +494,85 @@ def block_kv_cache(num_blocks: int, n_kv_heads: int, block_size: int, head_dim: 
     return BlockKVCache(k, v, ks, vs)
 
 
-def _require(ok, message: str):
-    if not ok:
-        raise ValueError(message)
-
-
-def _rows(x, name: str, dtype, device=None):
+def _rows(x, name: str, dtype, dev: int = -1) -> int:
     """Checks a matrix argument (CUDA, 2-D, unit column stride) and returns its row stride."""
-    _require(x.is_cuda and x.dtype == dtype and x.dim() == 2, f"{name} must be a 2-D {dtype} CUDA tensor")
-    _require(x.shape[1] <= 1 or x.stride(1) == 1, f"{name} must have unit column stride")
-    _require(device is None or x.device == device, f"{name} is on another device")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    shape, stride, at = x.shape, x.stride(), x.get_device()
+    if at < 0 or x.dtype != dtype or len(shape) != 2:
+        raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor")
+    if shape[1] > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if dev >= 0 and at != dev:
+        raise ValueError(f"{name} is on another device")
+    return stride[0] if shape[0] > 1 else shape[1]
 
 
-class _Call:
-    """Device and stream of one call: switches to the tensors' device when it is not the
-    current one, and tells the allocator about buffers allocated here that a stream other
-    than the current one uses."""
-
-    def __init__(self, device, stream, *allocated):
-        import torch
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        current = torch.cuda.current_stream(device)
-        if stream is not None and stream.cuda_stream != current.cuda_stream:
-            _require(stream.device == device, "stream is on another device")
-            for t in allocated:
-                t.record_stream(stream)
-            current = stream
-        self.stream = current.cuda_stream
-
-    def __call__(self, what, fn, *args):
-        if self.guard is not None:
-            with self.guard:
-                status = fn(*args, self.stream)
-        else:
-            status = fn(*args, self.stream)
-        if status != 0:
-            raise NVFP4Error(status, what)
-
-
-def _out_kind(out_dtype: str):
+def _launch(what: str, fn, dev: int, stream, made, *args):
+    """Calls an entry point with its device current, on ``stream`` (default: the device's
+    current one).  ``made``: buffers allocated by the caller, which the allocator has to
+    know of when another stream than the current one uses them."""
     import torch
-    _require(out_dtype in ("bf16", "f32"), f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
-    return (torch.bfloat16, 0) if out_dtype == "bf16" else (torch.float32, 1)
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is not None and stream.cuda_stream != raw:
+        if stream.device.index != dev:
+            raise ValueError("stream is on another device")
+        for t in made:
+            t.record_stream(stream)
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != 0:
+        raise NVFP4Error(status, what)
 
 
-def _cache_struct(cache: BlockKVCache, device) -> BlockCache:
+def _out_buffer(like, shape, out, out_dtype: str, made):
+    """(out, kind, row stride) of a BF16 or FP32 result of ``shape``, allocated when None."""
+    import torch
+    if out_dtype == "bf16":
+        dtype, kind = torch.bfloat16, 0
+    elif out_dtype == "f32":
+        dtype, kind = torch.float32, 1
+    else:
+        raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        made.append(out)
+        return out, kind, shape[1]
+    ld = _rows(out, "out", dtype, like.get_device())
+    if out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}")
+    return out, kind, ld
+
+
+def _cache_struct(cache: BlockKVCache, dev: int) -> BlockCache:
     import torch
     k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
-    _require(k.dim() == 4 and k.dtype == v.dtype == torch.uint8 and k.shape == v.shape, "cache k / v must be uint8 "
-             "[num_blocks, n_kv_heads, block_size, head_dim]")
-    nb, hk, block, d = k.shape
-    _require(ks.dtype == vs.dtype == torch.float32 and ks.shape == vs.shape == (nb, hk),
-             "cache scales must be float32 [num_blocks, n_kv_heads]")
-    _require(k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous(),
-             "cache tensors must be contiguous")
-    _require(k.device == v.device == ks.device == vs.device == device, "cache is on another device")
+    shape, u8, f32 = k.shape, torch.uint8, torch.float32
+    if len(shape) != 4 or k.dtype != u8 or v.dtype != u8 or v.shape != shape:
+        raise ValueError("cache k / v must be uint8 [num_blocks, n_kv_heads, block_size, head_dim]")
+    if ks.dtype != f32 or vs.dtype != f32 or ks.shape != shape[:2] or vs.shape != shape[:2]:
+        raise ValueError("cache scales must be float32 [num_blocks, n_kv_heads]")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache tensors must be contiguous")
+    if not k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == dev:
+        raise ValueError("cache is on another device")
+    nb, hk, block, d = shape
     return BlockCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), nb, block, hk, d)
 
 
-def _batch_struct(cu_seqlens, kv_lens, block_table, tokens, device) -> Batch:
+def _batch_struct(cu_seqlens, kv_lens, block_table, tokens: int, dev: int) -> Batch:
     import torch
     i32 = torch.int32
-    _require(cu_seqlens.dtype == kv_lens.dtype == block_table.dtype == i32,
-             "cu_seqlens, kv_lens and block_table must be int32")
-    _require(kv_lens.dim() == 1 and cu_seqlens.shape == (kv_lens.shape[0] + 1,) and block_table.dim() == 2
-             and block_table.shape[0] == kv_lens.shape[0], "cu_seqlens [n_seqs + 1], kv_lens [n_seqs] and block_table "
-             "[n_seqs, max_blocks] disagree")
-    _require(cu_seqlens.device == kv_lens.device == block_table.device == device, "batch tensors are on another device")
-    _require(cu_seqlens.is_contiguous() and kv_lens.is_contiguous(), "cu_seqlens and kv_lens must be contiguous")
-    ld = _rows(block_table, "block_table", i32)
+    ld = _rows(block_table, "block_table", i32, dev)
     n, cols = block_table.shape
+    if cu_seqlens.dtype != i32 or kv_lens.dtype != i32 or cu_seqlens.shape != (n + 1,) or kv_lens.shape != (n,):
+        raise ValueError("cu_seqlens must be int32 [n_seqs + 1] and kv_lens int32 [n_seqs], n_seqs the rows of block_table")
+    if not (cu_seqlens.is_contiguous() and kv_lens.is_contiguous()):
+        raise ValueError("cu_seqlens and kv_lens must be contiguous")
+    if cu_seqlens.get_device() != dev or kv_lens.get_device() != dev:
+        raise ValueError("cu_seqlens / kv_lens are on another device")
     return Batch(cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, tokens, cols, ld)
 
 
@@ -575,8 +581,8 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     p * base^(-2i / rot_dim) computed in FP64."""
     import torch
     table = torch.empty((max_positions, rot_dim), dtype=torch.float32, device=device)
-    _Call(table.device, stream, table)("nvfp4_rope_table", lib().nvfp4_rope_table, table.data_ptr(), max_positions,
-                                       rot_dim, float(base))
+    _launch("nvfp4_rope_table", lib().nvfp4_rope_table, table.get_device(), stream, (table,), table.data_ptr(),
+            max_positions, rot_dim, float(base))
     return table
 
 
@@ -591,36 +597,41 @@ def qk_norm_rope(q, k, w_q, w_k, positions=None, table=None, *, eps: float = 1e-
     Returns ``(q_out, k_out)``."""
     import torch
     bf16 = torch.bfloat16
-    ld_q = _rows(q, "q", bf16)
-    dev = q.device
+    ld_q, dev = _rows(q, "q", bf16), q.get_device()
     ld_k = _rows(k, "k", bf16, dev)
-    d, tokens = w_q.numel(), q.shape[0]
-    _require(w_q.dtype == w_k.dtype == bf16 and w_q.dim() == 1 and w_q.shape == w_k.shape and d > 0
-             and w_q.is_contiguous() and w_k.is_contiguous() and w_q.device == w_k.device == dev,
-             "w_q and w_k must be BF16 [head_dim] on q's device")
-    _require(k.shape[0] == tokens and q.shape[1] % d == 0 and k.shape[1] % d == 0, "q and k must have the same rows, "
-             "of whole heads")
-    rot, most = 0, 0
+    tokens, width_q = q.shape
+    d, width_k = w_q.numel(), k.shape[1]
+    if not (w_q.dtype == w_k.dtype == bf16 and w_q.dim() == 1 and w_q.shape == w_k.shape and d > 0
+            and w_q.is_contiguous() and w_k.is_contiguous() and w_q.get_device() == w_k.get_device() == dev):
+        raise ValueError("w_q and w_k must be BF16 [head_dim] on q's device")
+    if k.shape[0] != tokens or width_q % d or width_k % d:
+        raise ValueError("q and k must have the same rows, of whole heads")
+    rot = most = p_pos = p_table = 0
     if table is not None:
-        _require(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous() and table.device == dev,
-                 "table must be a contiguous float32 [max_positions, rot_dim] tensor on q's device")
+        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.get_device() != dev:
+            raise ValueError("table must be a contiguous float32 [max_positions, rot_dim] tensor on q's device")
+        if (positions is None or positions.dtype != torch.int64 or positions.shape != (tokens,)
+                or not positions.is_contiguous() or positions.get_device() != dev):
+            raise ValueError("positions must be a contiguous int64 [tokens] tensor on q's device")
         most, rot = table.shape
-        _require(positions is not None and positions.dtype == torch.int64 and positions.shape == (tokens,)
-                 and positions.is_contiguous() and positions.device == dev, "positions must be int64 [tokens]")
+        p_pos, p_table = positions.data_ptr(), table.data_ptr()
     made = []
     if q_out is None:
-        q_out = torch.empty((tokens, q.shape[1]), dtype=bf16, device=dev)
+        q_out, ld_qo = q.new_empty((tokens, width_q)), width_q
         made.append(q_out)
+    else:
+        ld_qo = _rows(q_out, "q_out", bf16, dev)
     if k_out is None:
-        k_out = torch.empty((tokens, k.shape[1]), dtype=bf16, device=dev)
+        k_out, ld_ko = q.new_empty((tokens, width_k)), width_k
         made.append(k_out)
-    ld_qo, ld_ko = _rows(q_out, "q_out", bf16, dev), _rows(k_out, "k_out", bf16, dev)
-    _require(q_out.shape == q.shape and k_out.shape == k.shape, "q_out / k_out must have the shape of q / k")
+    else:
+        ld_ko = _rows(k_out, "k_out", bf16, dev)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out / k_out must have the shape of q / k")
     if tokens:
-        _Call(dev, stream, *made)("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, q.data_ptr(), ld_q, k.data_ptr(), ld_k,
-                                  tokens, q.shape[1] // d, k.shape[1] // d, d, w_q.data_ptr(), w_k.data_ptr(),
-                                  weight_offset, eps, _ptr(positions), _ptr(table), most, rot, int(interleaved),
-                                  q_out.data_ptr(), ld_qo, k_out.data_ptr(), ld_ko)
+        _launch("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, dev, stream, made, q.data_ptr(), ld_q, k.data_ptr(),
+                ld_k, tokens, width_q // d, width_k // d, d, w_q.data_ptr(), w_k.data_ptr(), weight_offset, eps,
+                p_pos, p_table, most, rot, interleaved, q_out.data_ptr(), ld_qo, k_out.data_ptr(), ld_ko)
     return q_out, k_out
 
 
@@ -629,15 +640,15 @@ def kv_append(k, v, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, strea
     cache.  Sequence s has the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1, the last of its
     kv_lens[s] tokens (int32 tensors); block_table: int32 [n_seqs, max_blocks]."""
     import torch
-    ld_k = _rows(k, "k", torch.bfloat16)
-    dev = k.device
+    ld_k, dev = _rows(k, "k", torch.bfloat16), k.get_device()
     ld_v = _rows(v, "v", torch.bfloat16, dev)
+    tokens, width = k.shape
     c = _cache_struct(cache, dev)
-    _require(k.shape == v.shape and k.shape[1] == c.n_kv_heads * c.head_dim, "k and v must be [tokens, n_kv_heads * "
-             "head_dim] of the cache")
-    b = _batch_struct(cu_seqlens, kv_lens, block_table, k.shape[0], dev)
-    if k.shape[0] and b.n_seqs:
-        _Call(dev, stream)("nvfp4_kv_append", lib().nvfp4_kv_append, k.data_ptr(), ld_k, v.data_ptr(), ld_v, b, c)
+    if v.shape != k.shape or width != c.n_kv_heads * c.head_dim:
+        raise ValueError("k and v must be [tokens, n_kv_heads * head_dim] of the cache")
+    b = _batch_struct(cu_seqlens, kv_lens, block_table, tokens, dev)
+    if tokens and b.n_seqs:
+        _launch("nvfp4_kv_append", lib().nvfp4_kv_append, dev, stream, (), k.data_ptr(), ld_k, v.data_ptr(), ld_v, b, c)
 
 
 def attention_workspace_bytes(tokens: int, n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -653,32 +664,27 @@ def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softm
     least ``attention_workspace_bytes(...)`` bytes (allocated here when None); calls that
     share one must not overlap on the GPU.  Returns out [tokens, heads * head_dim]."""
     import torch
-    ld_q = _rows(q, "q", torch.bfloat16)
-    dev = q.device
-    c = _cache_struct(cache, dev)
+    ld_q, dev = _rows(q, "q", torch.bfloat16), q.get_device()
     tokens, width = q.shape
-    _require(c.head_dim > 0 and width % c.head_dim == 0, "q must be [tokens, heads * head_dim] of the cache")
-    heads = width // c.head_dim
+    c = _cache_struct(cache, dev)
+    d = c.head_dim
+    if d == 0 or width % d:
+        raise ValueError("q must be [tokens, heads * head_dim] of the cache")
     b = _batch_struct(cu_seqlens, kv_lens, block_table, tokens, dev)
-    dtype, kind = _out_kind(out_dtype)
     made = []
-    if out is None:
-        out = torch.empty((tokens, width), dtype=dtype, device=dev)
-        made.append(out)
-    ld_out = _rows(out, "out", dtype, dev)
-    _require(out.shape == q.shape, "out must have the shape of q")
+    out, kind, ld_out = _out_buffer(q, q.shape, out, out_dtype, made)
     if tokens == 0 or b.n_seqs == 0:
         return out
     L = lib()
     if workspace is None:
-        need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, heads, c.n_kv_heads, c.head_dim)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, width // d, c.n_kv_heads, d)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
         made.append(workspace)
-    _require(workspace.is_contiguous() and workspace.device == dev, "workspace must be contiguous, on q's device")
-    scale = c.head_dim ** -0.5 if softmax_scale is None else softmax_scale
-    _Call(dev, stream, *made)("nvfp4_attention", L.nvfp4_attention, q.data_ptr(), ld_q, heads, b, c, scale, int(causal),
-                              out.data_ptr(), kind, ld_out, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size())
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous, on q's device")
+    _launch("nvfp4_attention", L.nvfp4_attention, dev, stream, made, q.data_ptr(), ld_q, width // d, b, c,
+            d ** -0.5 if softmax_scale is None else softmax_scale, causal, out.data_ptr(), kind, ld_out,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -687,24 +693,22 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
     weight.  segments: list of ``(n_begin, n_end, gs_w)``; default one with ``w.gs``.
     Returns out [tokens, N] (BF16 or FP32)."""
     import torch
-    ld_x = _rows(x, "x", torch.bfloat16)
-    dev = x.device
-    _require(x.shape[1] == w.cols, "x must have the weight's columns")
-    _require(w.codes.device == w.scales.device == dev, "the weight is on another device")
-    dtype, kind = _out_kind(out_dtype)
+    ld_x, dev = _rows(x, "x", torch.bfloat16), x.get_device()
+    codes, scales, rows, cols = w.codes, w.scales, w.rows, w.cols
+    if x.shape[1] != cols:
+        raise ValueError("x must have the weight's columns")
+    if codes.get_device() != dev or scales.get_device() != dev:
+        raise ValueError("the weight is on another device")
     made = []
-    if out is None:
-        out = torch.empty((x.shape[0], w.rows), dtype=dtype, device=dev)
-        made.append(out)
-    ldo = _rows(out, "out", dtype, dev)
-    _require(out.shape == (x.shape[0], w.rows), "out must be [tokens, N]")
+    out, kind, ldo = _out_buffer(x, (x.shape[0], rows), out, out_dtype, made)
     if segments is None:
-        segments = ((0, w.rows, w.gs),)
-    _require(len(segments) <= MAX_SEGMENTS, "too many segments")
-    segs = (Segment * len(segments))(*[Segment(int(n0), int(n1), _ptr(g)) for n0, n1, g in segments])
-    _Call(dev, stream, *made)("nvfp4_matvec", lib().nvfp4_matvec, x.data_ptr(), ld_x, x.shape[0],
-                              Operand(w.codes.data_ptr(), w.scales.data_ptr(), w.rows, w.cols), segs, len(segments),
-                              out.data_ptr(), kind, ldo)
+        segments = ((0, rows, w.gs),)
+    n = len(segments)
+    if n > MAX_SEGMENTS:
+        raise ValueError("too many segments")
+    segs = (Segment * n)(*[Segment(n0, n1, _ptr(g)) for n0, n1, g in segments])
+    _launch("nvfp4_matvec", lib().nvfp4_matvec, dev, stream, made, x.data_ptr(), ld_x, x.shape[0],
+            Operand(codes.data_ptr(), scales.data_ptr(), rows, cols), segs, n, out.data_ptr(), kind, ldo)
     return out
 
 

@@ -6,7 +6,6 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -22,6 +21,7 @@
 #include "gdn_chunk.cuh"
 #include "layout.cuh"
 #include "attn_decode.cuh"
+#include "attn_prompt.cuh"
 #include "headnorm.cuh"
 #include "kvblock.cuh"
 #include "matvec.cuh"
@@ -83,6 +83,12 @@ nvfp4_status_t current_device(DeviceInfo **info) {
                              int(sizeof(gdn::Smem<32>))) != cudaSuccess ||
         cudaFuncSetAttribute(gdn::recurrence_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(sizeof(gdn::Smem<16>))) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::prompt::prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::prompt::smem_bytes<64>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::prompt::prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::prompt::smem_bytes<128>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::prompt::prompt_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::prompt::smem_bytes<256>()) != cudaSuccess ||
         cudaFuncSetAttribute(gdn::chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(sizeof(gdn::ChunkSmem))) != cudaSuccess)
       return NVFP4_ERR_CUDA;
@@ -310,6 +316,9 @@ nvfp4_status_t check_batch(const nvfp4_batch_t *b, const nvfp4_block_cache_t *c,
 
 // Workspace of nvfp4_attention: unit count, unit descriptors, partial results.
 constexpr int kMaxAttnCtas = 640;
+// Sequences with at most this many query rows per kv head (new tokens times heads of a
+// group) go to the decode kernel, the others to the prompt kernel.
+constexpr int kDecodeRows = 32;
 struct AttnWorkspace {
   int64_t units;
   size_t desc, desc2, part_ml, part, bytes;
@@ -317,7 +326,9 @@ struct AttnWorkspace {
 AttnWorkspace attn_workspace(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim) {
   AttnWorkspace w;
   const int64_t group = n_heads / n_kv_heads;
-  w.units = n_kv_heads * ((tokens * group + attn::kRows - 1) / attn::kRows + n_seqs);
+  const int64_t most = n_seqs * (kDecodeRows / attn::kRows);
+  w.units = (tokens * group + attn::kRows - 1) / attn::kRows + n_seqs;
+  w.units = n_kv_heads * (w.units < most ? w.units : most);
   w.desc = 256;
   w.desc2 = w.desc + w.units * sizeof(int4);
   w.part_ml = (w.desc2 + w.units * sizeof(int2) + 255) / 256 * 256;
@@ -1059,7 +1070,7 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   if (nvfp4_status_t st = check_batch(batch, cache, &log_block)) return st;
   if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || !std::isfinite(softmax_scale)) return NVFP4_ERR_INVALID_ARG;
   if (out_kind != NVFP4_OUT_BF16 && out_kind != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
-  if (n_heads > 65535) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (n_heads > 65535 || batch->tokens * (n_heads / cache->n_kv_heads) > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const int64_t width = int64_t(n_heads) * cache->head_dim;
   if (ld_q < width || ld_out < width) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(q_bf16, 16) || ld_q % 8 != 0 || !aligned(out, 16) || !aligned(workspace, 16) ||
@@ -1099,7 +1110,7 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   a.desc2 = reinterpret_cast<int2 *>(base + w.desc2);
   a.part_ml = reinterpret_cast<float2 *>(base + w.part_ml);
   a.part = reinterpret_cast<float *>(base + w.part);
-  a.max_decode_rows = INT_MAX;
+  a.max_decode_rows = kDecodeRows;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int i = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
   int ctas = dev->sms * dev->attn_ctas_per_sm[i];
@@ -1107,7 +1118,22 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   auto kernel = i == 0 ? attn::decode_kernel<64> : i == 1 ? attn::decode_kernel<128> : attn::decode_kernel<256>;
   auto combine = i == 0 ? attn::combine_kernel<64> : i == 1 ? attn::combine_kernel<128> : attn::combine_kernel<256>;
   if (nvfp4_status_t e = launch_pdl(kernel, dim3(ctas), dim3(attn::kThreads), 0, s, 1, a)) return e;
-  return launch_pdl(combine, dim3(static_cast<unsigned>(w.units), attn::kRows), dim3(cache->head_dim / 2), 0, s, 1, a);
+  if (nvfp4_status_t e = launch_pdl(combine, dim3(static_cast<unsigned>(w.units), attn::kRows),
+                                    dim3(cache->head_dim / 2), 0, s, 1, a))
+    return e;
+  // Only the device knows the sequences' lengths; no prompt fits in few rows.
+  const int64_t rows = batch->tokens * a.group;
+  if (rows <= kDecodeRows) return NVFP4_OK;
+  auto launch_prompt = [&](auto kernel, int tile_rows, int smem) {
+    const int64_t items = (rows / tile_rows + batch->n_seqs) * a.kv_heads;
+    if (items > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(attn::prompt::kThreads), smem, s, 1, a);
+  };
+  if (i == 0)
+    return launch_prompt(attn::prompt::prompt_kernel<64>, attn::prompt::Cfg<64>::ROWS, attn::prompt::smem_bytes<64>());
+  if (i == 1)
+    return launch_prompt(attn::prompt::prompt_kernel<128>, attn::prompt::Cfg<128>::ROWS, attn::prompt::smem_bytes<128>());
+  return launch_prompt(attn::prompt::prompt_kernel<256>, attn::prompt::Cfg<256>::ROWS, attn::prompt::smem_bytes<256>());
 }
 
 nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const nvfp4_operand_t *W,
