@@ -5,4 +5,4 @@ reference arm may import this package.  It shares no code with the CUDA library
 (``nvfp4_w4a4_quantized_02_b200``) and never imports it.
 """
 from .nvfp4_oracle import *  # noqa: F401,F403
-from . import layout  # noqa: F401
+from . import attention, layout  # noqa: F401
