@@ -299,8 +299,9 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int e = row_exponent(amax);
-    // two factors: 2^-e alone can leave FP32's range
-    const float f0 = ldexpf(1.0f, -(e / 2)), f1 = ldexpf(1.0f, -(e - e / 2));
+    // two factors: 2^-e alone can leave FP32's range.  An infinite value makes every score of the
+    // row infinite or NaN: the row is NaN.
+    const float f0 = amax <= 3.4e38f ? ldexpf(1.0f, -(e / 2)) : __int_as_float(0x7fffffff), f1 = ldexpf(1.0f, -(e - e / 2));
 #pragma unroll
     for (int i = 0; i < C::SEGK; ++i)
 #pragma unroll

@@ -2,21 +2,27 @@
 // attn_decode.cuh on tcgen05 with tiles of 128 query rows.
 //
 // A query row is one head of one token; the rows of a kv head's group are numbered token by
-// token, so 128 rows of a tile share every cached byte.  K and V codes are exact in FP16:
-// converter warps turn a tile of codes into FP16 in shared memory (rows of tokens in panels of
-// 64 values, 128-byte swizzle), where K is a K-major and V, in the same layout, an MN-major
-// operand.  S = Q K^T accumulates in TMEM; a softmax warpgroup reads it one row per thread,
-// writes P over it as FP16, and O += P V takes P from TMEM.  O stays in TMEM and is rescaled
-// only when a row's maximum has grown by more than 2^kSlack since its reference was set
-// (weights are at most 2^(kSlack + kBoost), within FP16).
+// token, so 128 rows of a tile share every cached byte.
+//  * S = Q K^T runs on the codes themselves: K goes by TMA straight into its operand layout,
+//    and q, scaled by a power of two per row, is the sum of two E4M3 parts, hi = E4M3(q) and
+//    lo = E4M3(q - hi).  A BF16 value has 8 significant bits and each part holds 4, so the sum is exact
+//    down to 2^-10 of the row's largest value (and to 2^-18 of it in absolute terms below).  Two FP8
+//    products cost what one in FP16 would, and K needs no conversion.
+//  * O += P V runs in FP16, since P needs more than 8 bits of range and precision: a converter
+//    warpgroup turns V codes (exact in FP16) into panels of 64 values with 128-byte swizzle,
+//    token rows, which the product reads as an MN-major operand.
+// S accumulates in TMEM; a softmax warpgroup reads it one row per thread and writes P over it as
+// FP16, the A operand of O += P V.  O stays in TMEM and is rescaled only when a row's maximum has
+// grown by more than 2^kSlack since its reference was set (weights are at most
+// 2^(kSlack + kBoostP), within FP16).
 //
 // Two streams keep the tensor cores busy while the other's softmax runs.  Up to 128 values per
 // head they are two tiles of query rows with their own O over the same K / V tiles of 128
 // tokens; at 256 values TMEM holds one O, and the streams are the even and odd K / V tiles of
 // 64 tokens, which hand the rows' reference maxima to each other.
 //
-// Warps (one CTA per SM): 0-3 and 4-7 softmax of stream 0 and 1, 8-11 K converters,
-// 12-15 V converters, 16 MMA issuer.
+// Warps (one CTA per SM): 0-3 and 4-7 softmax of stream 0 and 1, 8-11 V converter, 12 MMA
+// issuer, 13 producer (block table, scales, copies).
 #pragma once
 
 #include "attn_decode.cuh"
@@ -25,7 +31,7 @@ namespace nvfp4 {
 namespace attn {
 namespace prompt {
 
-constexpr int kThreads = 544;
+constexpr int kThreads = 448;
 constexpr int kTile = 128;      // query rows of a tile
 constexpr float kSlack = 8.0f;
 constexpr float kBoostP = 6.0f;
@@ -35,16 +41,22 @@ struct Cfg {
   static constexpr bool kSplitKV = D == 256;           // streams are K / V tiles, not row tiles
   static constexpr int NQ = kSplitKV ? 1 : 2;
   static constexpr int BN = kSplitKV ? 64 : 128;       // cached tokens of a tile
-  static constexpr int PANELS = D / 64;
-  static constexpr int Q_BYTES = NQ * kTile * D * 2;
-  static constexpr int KV_BYTES = BN * D * 2;
-  static constexpr int STAGES = 2;
+  static constexpr int ROWB = D < 128 ? D : 128;       // bytes of a row of a panel of codes
+  static constexpr int PANELS8 = D / ROWB;             // panels of codes
+  static constexpr int Q_PART = kTile * D;             // one part of one query tile
+  static constexpr int Q_BYTES = NQ * 2 * Q_PART;
+  static constexpr int K_BYTES = BN * D;
+  static constexpr int V_BYTES = BN * D * 2;
+  static constexpr int K_STAGES = 3;
   static constexpr int GROUPS = BN / kGroup;
   static constexpr int CPR = D / 16;                   // 16-byte pieces of a row of codes
   static constexpr int PIECES = BN * CPR / 128;        // per converter thread
   static constexpr int ROWS = NQ * kTile;
   static constexpr int S_COL = BN;                     // TMEM columns of one S
   static constexpr int O_COL0 = 256;
+  // shared memory: Q, K stages, V (FP16) x 2, V codes x 2
+  static constexpr int K_OFF = Q_BYTES, V_OFF = K_OFF + K_STAGES * K_BYTES, RAW_OFF = V_OFF + 2 * V_BYTES,
+                       CTL_OFF = RAW_OFF + 2 * K_BYTES;
 };
 
 struct Scales {
@@ -53,12 +65,15 @@ struct Scales {
 
 template <int D>
 struct Control {
-  uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_empty[2], s_ready[2], p_ready[2], o_done[2], m_ready[2], join, done;
+  uint64_t q_ready, k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2], s_ready[2], p_ready[2],
+      o_done[2], m_ready[2], join, done;
   uint32_t tmem;
   int nan_any;
-  // A tile's scales, written with its K.  Its slot comes up again four tiles later, when the
-  // products with the earlier tile's weights have been issued: its readers are done.
-  Scales ks[4][Cfg<D>::GROUPS];
+  // Scales and the mask of the groups that hold tokens, by tile.  A slot comes up again eight
+  // tiles later; a tile's K is loaded at most three tiles ahead of the products with K, and those
+  // are issued at most two tiles ahead of the last softmax that is not done.
+  Scales ks[8][Cfg<D>::GROUPS];
+  uint32_t valid[8];
   int nan_first[D];
   float m_ref[kTile];            // kSplitKV: reference maxima of the rows
   float l[2][kTile];
@@ -66,19 +81,20 @@ struct Control {
 
 template <int D>
 constexpr int smem_bytes() {
-  return 1024 + Cfg<D>::Q_BYTES + 2 * Cfg<D>::STAGES * Cfg<D>::KV_BYTES + int(sizeof(Control<D>));
+  return 1024 + Cfg<D>::CTL_OFF + int(sizeof(Control<D>));
 }
 
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+__host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
-// FP16 MMA with FP32 accumulation, A from shared memory / from TMEM.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// FP8 MMA, both operands E4M3 in shared memory, and FP16 MMA with A in TMEM; FP32 accumulation.
+// (The E4M3 codes of the descriptor's type fields are 0, as are FP16's.)
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -101,6 +117,26 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mnmajor(uint32_t saddr, uint32_t
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
+}
+
+// K-major operand whose rows are 64 bytes, with the 64-byte swizzle; 8-row groups 512 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw64_kmajor(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(512 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -130,6 +166,13 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // 16-byte piece `c` (of 8) of row `r` of panel `p`, a panel holding `rows` rows.
 __device__ __forceinline__ uint32_t panel_offset(int rows, int p, int r, int c) {
   return (p * rows + r) * 128 + ((c ^ (r & 7)) << 4);
+}
+
+// The same for rows of codes: panels of ROWB bytes.
+template <int D>
+__device__ __forceinline__ uint32_t code_offset(int rows, int r, int c) {
+  if constexpr (D < 128) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  return ((c >> 3) * rows + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // What a CTA works on.
@@ -195,60 +238,111 @@ __device__ bool find_item(const Args &a, Item &it) {
   return false;
 }
 
-// Converter warpgroup (tid 0..127) of K or of V.
-template <int D, bool V>
-__device__ void convert(const Args &a, Control<D> &c, unsigned char *buf, const Item &it, int n_tiles, int tid) {
+// Producer warp.  A tile consists of BN / R boxes of R consecutive tokens of one cache block
+// (R = min(block size, BN)); lane i looks up, and copies, box i.
+template <int D>
+__device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, unsigned char *kbuf, unsigned char *raw,
+                        const Item &it, int n_tiles) {
   using C = Cfg<D>;
-  const int lane = tid & 31;
-  const uint8_t *src = V ? a.v : a.k;
-  // lane i < GROUPS of every warp knows the (block, head) index of the tile's group i
-  auto blocks_of = [&](int j) -> int64_t {
-    if (j >= n_tiles || lane >= C::GROUPS) return -1;
-    return group_block<D>(a, it.seq, it.h, j * C::BN + lane * kGroup, it.kv_end);
-  };
-  uint4 raw[C::PIECES];
-  auto load = [&](int j, int64_t blk) {
-#pragma unroll
-    for (int i = 0; i < C::PIECES; ++i) {
-      const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR;
-      const int64_t b = __shfl_sync(0xffffffffu, blk, row / kGroup);
-      const int tok = j * C::BN + row;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (b >= 0 && tok < it.kv_end)
-        raw[i] = ld_stream(src + ((b << a.log_block) + (tok & ((1 << a.log_block) - 1))) * D + 16 * col);
+  const int lane = threadIdx.x & 31;
+  const int log_r = min(a.log_block, C::kSplitKV ? 6 : 7), R = 1 << log_r, boxes = C::BN >> log_r;
+  const int mask = (1 << a.log_block) - 1;
+  const int32_t *row = a.table + it.seq * a.ld_table;
+  auto token = [&](int j) { return j * C::BN + (lane << log_r); };
+  auto wanted = [&](int j) { return j < n_tiles && lane < boxes && token(j) < it.kv_end; };
+  auto lookup = [&](int j) { return wanted(j) ? __ldg(row + (token(j) >> a.log_block)) : -1; };
+  auto check = [&](int j, int id) -> int {  // (block, head) index, -1: nothing there
+    if (!wanted(j)) return -1;
+    if (id < 0 || id >= a.num_blocks) {
+      record_bad_index();
+      return -1;
     }
+    return id * a.kv_heads + it.h;
   };
-  int64_t blk = blocks_of(0);
-  load(0, blk);
-  int64_t next = blocks_of(1);
+  int blk = check(0, lookup(0)), next_id = lookup(1);
+  float sk = blk >= 0 ? __ldg(a.k_scales + blk) : 0.0f, sv = blk >= 0 ? __ldg(a.v_scales + blk) : 1.0f;
+#pragma unroll 1
   for (int j = 0; j < n_tiles; ++j) {
-    const int st = j & 1;
-    if (!mbar_wait(V ? &c.v_empty[st] : &c.k_empty[st], ((j >> 1) & 1) ^ 1)) return;
-    if (!V && tid < C::GROUPS) {  // tid == lane here
+    const int ks = j % C::K_STAGES, rs = j & 1;
+    const uint32_t have = __ballot_sync(0xffffffffu, blk >= 0);
+    const uint32_t bytes = __popc(have) * (R * D);
+    if (!mbar_wait(&c.k_empty[ks], ((j / C::K_STAGES) & 1) ^ 1)) return;
+    if (lane < boxes) {
       Scales s;
-      s.k = blk >= 0 ? __ldg(a.k_scales + blk) : 0.0f;
-      s.log_v = blk >= 0 ? log_scale(__ldg(a.v_scales + blk)) : -INFINITY;  // no such block: nothing to see
+      s.k = sk;
+      s.log_v = blk >= 0 ? log_scale(sv) : -INFINITY;  // no such block: nothing to see
       s.inv_v = blk >= 0 ? exp2f(-s.log_v) : 0.0f;
       s.pad = 0.0f;
-      c.ks[j & 3][tid] = s;
+      for (int g = 0; g < R / kGroup; ++g) c.ks[j & 7][lane * (R / kGroup) + g] = s;
     }
-    unsigned char *dst = buf + st * C::KV_BYTES;
-    const bool partial = V && (j + 1) * C::BN > it.lim_min;
+    if (lane == 0) c.valid[j & 7] = have;
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(&c.k_full[ks], bytes);
+    __syncwarp();
+    const int tok = token(j);
+    if (blk >= 0) {
 #pragma unroll
-    for (int i = 0; i < C::PIECES; ++i) {
-      const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR;
-      uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      if (partial) {  // a NaN that some rows must not see: see decode_segment
+      for (int p = 0; p < C::PANELS8; ++p)
+        tma_load_3d(kbuf + ks * C::K_BYTES + (p * C::BN + lane * R) * C::ROWB, k_map, &c.k_full[ks], p * 128, tok & mask, blk);
+    }
+    if (!mbar_wait(&c.raw_empty[rs], ((j >> 1) & 1) ^ 1)) return;
+    if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[rs], bytes);
+    __syncwarp();
+    if (blk >= 0)
+      bulk_load(raw + rs * C::K_BYTES + lane * R * D, a.v + ((int64_t(blk) << a.log_block) + (tok & mask)) * D, R * D,
+                &c.raw_full[rs]);
+    blk = check(j + 1, next_id);
+    sk = blk >= 0 ? __ldg(a.k_scales + blk) : 0.0f;
+    sv = blk >= 0 ? __ldg(a.v_scales + blk) : 1.0f;
+    next_id = lookup(j + 2);
+  }
+}
+
+// Converter warpgroup (tid 0..127): tile after tile of V codes into FP16.
+template <int D>
+__device__ void convert(const Args &a, Control<D> &c, const unsigned char *raw, unsigned char *vbuf, const Item &it,
+                        int n_tiles, int tid) {
+  using C = Cfg<D>;
+  const int log_r = min(a.log_block, C::kSplitKV ? 6 : 7);
+  const uint32_t all = C::BN >> log_r == 32 ? 0xffffffffu : (1u << (C::BN >> log_r)) - 1;
+#pragma unroll 1
+  for (int j = 0; j < n_tiles; ++j) {
+    const int st = j & 1;
+    const uint32_t phase = (j >> 1) & 1;
+    if (!mbar_wait(&c.raw_full[st], phase)) return;
+    const uint32_t have = c.valid[j & 7];
+    uint4 x[C::PIECES];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+    for (int i = 0; i < C::PIECES; ++i)
+      x[i] = *reinterpret_cast<const uint4 *>(raw + st * C::K_BYTES + (tid + 128 * i) * 16);
+    mbar_arrive(&c.raw_empty[st]);
+    if (have != all || (j + 1) * C::BN > it.lim_min) {
+#pragma unroll
+      for (int i = 0; i < C::PIECES; ++i) {
+        const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR, tok = j * C::BN + row;
+        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const bool gone = !((have >> (row >> log_r)) & 1) || tok >= it.kv_end;  // bytes that belong to no token
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (gone) w[k] = 0;
+          // a NaN that some rows must not see: see decode_segment
           if (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u)
             for (int b = 0; b < 4; ++b)
               if (((w[k] >> (8 * b)) & 0x7f) == 0x7f) {
-                atomicMin(&c.nan_first[16 * col + 4 * k + b], j * C::BN + row);
+                atomicMin(&c.nan_first[16 * col + 4 * k + b], tok);
                 c.nan_any = 1;
                 w[k] &= ~(0xffu << (8 * b));
               }
+        }
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+    }
+    if (!mbar_wait(&c.v_empty[st], phase ^ 1)) return;
+    unsigned char *dst = vbuf + st * C::V_BYTES;
+#pragma unroll
+    for (int i = 0; i < C::PIECES; ++i) {
+      const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint4 h[2];
       h[0] = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]), e4m3x2_to_f16x2(w[1] >> 16));
       h[1] = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]), e4m3x2_to_f16x2(w[3] >> 16));
@@ -258,10 +352,7 @@ __device__ void convert(const Args &a, Control<D> &c, unsigned char *buf, const 
       *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + (o ^ 1))) = o ? h[0] : h[1];
     }
     fence_async_smem();
-    mbar_arrive(V ? &c.v_full[st] : &c.k_full[st]);
-    blk = next;
-    load(j + 1, blk);
-    next = blocks_of(j + 2);
+    mbar_arrive(&c.v_full[st]);
   }
 }
 
@@ -269,36 +360,43 @@ __device__ void convert(const Args &a, Control<D> &c, unsigned char *buf, const 
 template <int D>
 __device__ void issue(Control<D> &c, uint32_t tmem, uint32_t q, uint32_t k, uint32_t v, int n_tiles) {
   using C = Cfg<D>;
-  constexpr uint32_t kIdescS = idesc_f16(kTile, C::BN, false), kIdescO = idesc_f16(kTile, D, true);
-  auto qk = [&](int w, int j) {  // stream w's S = Q K_j^T
-    const uint32_t qa = q + (C::kSplitKV ? 0 : w * kTile * D * 2), ka = k + (j & 1) * C::KV_BYTES;
+  constexpr uint32_t kIdescS = make_idesc(kTile, C::BN, false), kIdescO = make_idesc(kTile, D, true);
+  auto desc = [](uint32_t at) { return D < 128 ? sdesc_sw64_kmajor(at) : sdesc_sw128_kmajor(at); };
+  auto qk = [&](int w, int j) {  // stream w's S = (hi + lo) K_j^T
+    const uint32_t qa = q + (C::kSplitKV ? 0 : w * 2 * C::Q_PART), ka = k + (j % C::K_STAGES) * C::K_BYTES;
 #pragma unroll
-    for (int p = 0; p < C::PANELS; ++p) {
-      const uint64_t ad = sdesc_sw128_kmajor(qa + p * kTile * 128), bd = sdesc_sw128_kmajor(ka + p * C::BN * 128);
+    for (int part = 0; part < 2; ++part)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) mma_f16_ss(tmem + w * C::S_COL, ad + 2 * s, bd + 2 * s, kIdescS, (p | s) != 0);
-    }
+      for (int p = 0; p < C::PANELS8; ++p) {
+        const uint64_t ad = desc(qa + part * C::Q_PART + p * kTile * 128), bd = desc(ka + p * C::BN * 128);
+#pragma unroll
+        for (int s = 0; s < C::ROWB / 32; ++s)
+          mma_f8_ss(tmem + w * C::S_COL, ad + 2 * s, bd + 2 * s, kIdescS, (part | p | s) != 0);
+      }
     tc_commit(&c.s_ready[w]);
   };
   auto pv = [&](int w, int j) {  // O += P V_j
-    const uint32_t va = v + (j & 1) * C::KV_BYTES;
+    const uint32_t va = v + (j & 1) * C::V_BYTES;
     const uint32_t o = tmem + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
 #pragma unroll
     for (int s = 0; s < C::BN / 16; ++s)
       mma_f16_ts(o, tmem + w * C::S_COL + 8 * s, sdesc_sw128_mnmajor(va + s * 2048, C::BN * 128), kIdescO, (j | s) != 0);
     tc_commit(&c.o_done[w]);
   };
-  auto full = [&](uint64_t *b, int j) { return mbar_wait(&b[j & 1], (j >> 1) & 1); };
+  auto k_full = [&](int j) { return mbar_wait(&c.k_full[j % C::K_STAGES], (j / C::K_STAGES) & 1); };
+  auto k_done = [&](int j) { tc_commit(&c.k_empty[j % C::K_STAGES]); };
+  auto v_full = [&](int j) { return mbar_wait(&c.v_full[j & 1], (j >> 1) & 1); };
 
   if (!mbar_wait(&c.q_ready, 0)) return;
   if constexpr (!C::kSplitKV) {
-    if (!full(c.k_full, 0)) return;
+    if (!k_full(0)) return;
     tc_fence_after();
     qk(0, 0);
     qk(1, 0);
-    tc_commit(&c.k_empty[0]);
+    k_done(0);
+#pragma unroll 1
     for (int j = 0; j < n_tiles; ++j) {
-      if (!full(c.v_full, j)) return;
+      if (!v_full(j)) return;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (!mbar_wait(&c.p_ready[w], j & 1)) return;
@@ -306,31 +404,32 @@ __device__ void issue(Control<D> &c, uint32_t tmem, uint32_t q, uint32_t k, uint
         pv(w, j);
         if (w == 1) tc_commit(&c.v_empty[j & 1]);
         if (j + 1 < n_tiles) {
-          if (w == 0 && !full(c.k_full, j + 1)) return;
+          if (w == 0 && !k_full(j + 1)) return;
           tc_fence_after();
           qk(w, j + 1);
-          if (w == 1) tc_commit(&c.k_empty[(j + 1) & 1]);
+          if (w == 1) k_done(j + 1);
         }
       }
     }
   } else {
     for (int j = 0; j < 2 && j < n_tiles; ++j) {
-      if (!full(c.k_full, j)) return;
+      if (!k_full(j)) return;
       tc_fence_after();
       qk(j, j);
-      tc_commit(&c.k_empty[j]);
+      k_done(j);
     }
+#pragma unroll 1
     for (int j = 0; j < n_tiles; ++j) {
       const int w = j & 1;
-      if (!full(c.v_full, j) || !mbar_wait(&c.p_ready[w], (j >> 1) & 1)) return;
+      if (!v_full(j) || !mbar_wait(&c.p_ready[w], (j >> 1) & 1)) return;
       tc_fence_after();
       pv(w, j);
       tc_commit(&c.v_empty[w]);
       if (j + 2 < n_tiles) {
-        if (!full(c.k_full, j + 2)) return;
+        if (!k_full(j + 2)) return;
         tc_fence_after();
         qk(w, j + 2);
-        tc_commit(&c.k_empty[w]);
+        k_done(j + 2);
       }
     }
   }
@@ -351,6 +450,130 @@ __device__ __forceinline__ void scale_o(uint32_t o, float f) {
   tmem_st_wait();
 }
 
+__device__ __forceinline__ float fmaxf_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// 2^x for two values on the FMA pipe: 2^n 2^f with n = round(x), f in [-1/2, 1/2], and a
+// polynomial of degree 4 for 2^f (minimax in relative error by Remez' exchange, 2^-18.5, far
+// below the FP16 rounding that follows).  x >= -126 after clamping; not for NaN.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves round(x) in the low bits
+  x.x = fmaxf(x.x, -126.0f);
+  x.y = fmaxf(x.y, -126.0f);
+  const float2 t = add_f32x2(x, make_float2(kMagic, kMagic));
+  const float2 n = add_f32x2(t, make_float2(-kMagic, -kMagic));
+  const float2 f = fma_f32x2(n, make_float2(-1.0f, -1.0f), x);
+  float2 p = fma_f32x2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+                       make_float2(0.05591785907745361f, 0.05591785907745361f));
+  p = fma_f32x2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  p = fma_f32x2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  p = fma_f32x2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// Maximum of x = s c + e over the thread's row of S, NaN if there is one; MASK: only the first `vis` columns.
+template <int D, bool MASK>
+__device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, float rc, int vis) {
+  using C = Cfg<D>;
+  constexpr int N = C::BN / 32;
+  float mt = -INFINITY;
+  uint32_t r[2][32];
+  tmem_ld_32x32b_x32(s_tmem, r[0]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t(&v)[32] = r[i & 1];
+    tmem_ld_wait();
+    if (i + 1 < N) tmem_ld_32x32b_x32(s_tmem + 32 * (i + 1), r[(i + 1) & 1]);
+    if constexpr (MASK) {
+#pragma unroll
+      for (int n = 0; n < 32; ++n)
+        if (32 * i + n >= vis) v[n] = 0xff800000u;
+    }
+    float m[2][2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t *u = v + 16 * g;
+      m[g][0] = fmaxf_nan(__uint_as_float(u[0]), __uint_as_float(u[1]));
+      m[g][1] = fmaxf_nan(__uint_as_float(u[2]), __uint_as_float(u[3]));
+#pragma unroll
+      for (int n = 4; n < 16; n += 4) {
+        m[g][0] = max3(m[g][0], __uint_as_float(u[n]), __uint_as_float(u[n + 1]));
+        m[g][1] = max3(m[g][1], __uint_as_float(u[n + 2]), __uint_as_float(u[n + 3]));
+      }
+      const float x = fmaxf_nan(m[g][0], m[g][1]);
+      const Scales s = sc[2 * i + g];
+      const float y = fmaf(x, s.k * rc, s.log_v);
+      mt = fmaxf_nan(mt, x == -INFINITY ? x : y);
+    }
+  }
+  return mt;
+}
+
+// P = 2^(x - base) over S, as FP16; returns sum of P / sV.
+template <int D, bool MASK>
+__device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, float rc, float base, int vis) {
+  using C = Cfg<D>;
+  constexpr int N = C::BN / 32;
+  float l = 0.0f;
+  uint32_t r[2][32];
+  tmem_ld_32x32b_x32(s_tmem, r[0]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t(&v)[32] = r[i & 1];
+    tmem_ld_wait();
+    if (i + 1 < N) tmem_ld_32x32b_x32(s_tmem + 32 * (i + 1), r[(i + 1) & 1]);
+    uint32_t p[16];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const Scales s = sc[2 * i + g];
+      const float ck = s.k * rc, ce = s.log_v - base;
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int n = 0; n < 16; n += 2) {
+        float2 x = fma_f32x2(make_float2(__uint_as_float(v[16 * g + n]), __uint_as_float(v[16 * g + n + 1])),
+                             make_float2(ck, ck), make_float2(ce, ce));
+        if constexpr (MASK) {
+          if (32 * i + 16 * g + n >= vis) x.x = -INFINITY;
+          if (32 * i + 16 * g + n + 1 >= vis) x.y = -INFINITY;
+        }
+        // one pair in four on the FMA pipe: the MUFU's 16 exponentials per clock are the bound
+        if (n % 8 == 6) {
+          x = exp2_poly(x);
+        } else {
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+        }
+        sum = add_f32x2(sum, x);
+        p[8 * g + n / 2] = pack_f16(x.x, x.y);
+      }
+      l = fmaf(sum.x + sum.y, s.inv_v, l);
+    }
+    tmem_st_32x32b_x16(s_tmem + 16 * i, p);
+  }
+  return l;
+}
+
 // Softmax warpgroup of stream w; tid 0..127 is the row of its tile.
 template <int D>
 __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned char *qbuf, const Item &it, int n_tiles,
@@ -363,7 +586,7 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
   const int lim = !valid ? it.kv_end : a.causal ? it.sq.kv_len - it.sq.q_len + tok + 1 : it.sq.kv_len;
   const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
 
-  // This thread's Q row as FP16, scaled by 2^-e (both streams of kSplitKV need e; the second
+  // This thread's Q row in two E4M3 parts, scaled by 2^-e (both streams of kSplitKV need e; each
   // writes half of the row).
   float rc;
   {
@@ -377,21 +600,41 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
       for (int n = 0; n < 4; ++n)
         amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[n] << 16)), fabsf(__uint_as_float(v[n] & 0xFFFF0000u))));
     }
-    const int e = valid ? row_exponent(amax) : 0;
-    const float f0 = valid ? ldexpf(a.scale_log2 < 0.0f ? -1.0f : 1.0f, -(e / 2)) : 0.0f, f1 = ldexpf(1.0f, -(e - e / 2));
-    rc = ldexpf(fabsf(a.scale_log2), e);
-    unsigned char *q = qbuf + (C::kSplitKV ? 0 : w * kTile * D * 2);
-    constexpr int kHalf = C::kSplitKV ? D / 16 : D / 8;
-    const int first = C::kSplitKV ? w * kHalf : 0;
-#pragma unroll 4
-    for (int i = first; i < first + kHalf; ++i) {
-      const uint4 x = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
-      const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[4];
+    const int e = row_exponent(amax) + 6;  // largest magnitude in [2^8, 2^9); see below
+    // magnitudes above 448 = 1.75 * 2^8 take one more halving
+    const int ee = amax > 448.0f * ldexpf(1.0f, min(e, 118)) && amax <= 3.4e38f ? e + 1 : e;
+    // an infinite value makes every score of the row infinite or NaN: the row is NaN
+    const float f0 = !valid ? 0.0f : amax <= 3.4e38f ? ldexpf(a.scale_log2 < 0.0f ? -1.0f : 1.0f, -(ee / 2)) : __int_as_float(0x7fffffff);
+    const float f1 = ldexpf(1.0f, -(ee - ee / 2));
+    rc = ldexpf(fabsf(a.scale_log2), ee);
+    unsigned char *hi = qbuf + (C::kSplitKV ? 0 : w * 2 * C::Q_PART), *lo = hi + C::Q_PART;
+    constexpr int kPieces = C::kSplitKV ? D / 32 : D / 16;
+    const int first = C::kSplitKV ? w * kPieces : 0;
+#pragma unroll 2
+    for (int i = first; i < first + kPieces; ++i) {  // 16 values
+      uint32_t oh[4], ol[4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        o[n] = pack_f16(__uint_as_float(v[n] << 16) * f0 * f1, __uint_as_float(v[n] & 0xFFFF0000u) * f0 * f1);
-      *reinterpret_cast<uint4 *>(q + panel_offset(kTile, i >> 3, tid, i & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int k = 0; k < 2; ++k) {
+        const uint4 x = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + 2 * i + k) : make_uint4(0, 0, 0, 0);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int n = 0; n < 4; n += 2) {
+          uint32_t h = 0, l8 = 0;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const float x0 = __uint_as_float(v[n + m] << 16) * f0 * f1, x1 = __uint_as_float(v[n + m] & 0xFFFF0000u) * f0 * f1;
+            const uint32_t c8 = cvt_e4m3x2(x1, x0);
+            const uint32_t back = e4m3x2_to_f16x2(c8);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+            h |= c8 << (16 * m);
+            l8 |= static_cast<uint32_t>(cvt_e4m3x2(x1 - hf.y, x0 - hf.x)) << (16 * m);
+          }
+          oh[2 * k + n / 2] = h;
+          ol[2 * k + n / 2] = l8;
+        }
+      }
+      *reinterpret_cast<uint4 *>(hi + code_offset<D>(kTile, tid, i)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+      *reinterpret_cast<uint4 *>(lo + code_offset<D>(kTile, tid, i)) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
     }
     fence_async_smem();
     mbar_arrive(&c.q_ready);
@@ -401,35 +644,16 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
   const uint32_t s_tmem = tmem + lanes + w * C::S_COL, o_tmem = tmem + lanes + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
   float m_ref = -INFINITY, l = 0.0f;
   const int steps = C::kSplitKV ? (n_tiles - w + 1) / 2 : n_tiles;
+#pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     const int j = C::kSplitKV ? 2 * i + w : i;
     if (!mbar_wait(&c.s_ready[w], i & 1)) return;
     tc_fence_after();
-    const Scales *sc = c.ks[j & 3];
+    const Scales *sc = c.ks[j & 7];
     const int vis = lim - j * C::BN;  // visible columns of this row
     const bool masked = warp_lim < (j + 1) * C::BN;
 
-    // maximum of x = s c + e over the row
-    float mt = -INFINITY;
-#pragma unroll
-    for (int c0 = 0; c0 < C::BN; c0 += 32) {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(s_tmem + c0, r);
-      tmem_ld_wait();
-      if (masked) {
-#pragma unroll
-        for (int n = 0; n < 32; ++n)
-          if (c0 + n >= vis) r[n] = 0xff800000u;
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) x = fmaxf(x, __uint_as_float(r[16 * g + n]));
-        const Scales s = sc[c0 / 16 + g];
-        mt = fmaxf(mt, x == -INFINITY ? x : fmaf(x, s.k * rc, s.log_v));
-      }
-    }
+    const float mt = masked ? row_max<D, true>(s_tmem, sc, rc, vis) : row_max<D, false>(s_tmem, sc, rc, vis);
 
     if constexpr (C::kSplitKV) {
       if (j > 0) {
@@ -439,6 +663,7 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
         m_ref = m;
       }
     }
+    if (!(mt < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or infinite score: so is the row
     const bool grow = mt > m_ref + kSlack || (m_ref == -INFINITY && mt > m_ref);
     if (__any_sync(0xffffffffu, grow)) {
       const float f = grow ? ex2(m_ref - mt) : 1.0f;
@@ -460,32 +685,7 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
     }
 
     const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kBoostP;
-#pragma unroll
-    for (int c0 = 0; c0 < C::BN; c0 += 32) {
-      uint32_t r[32], p[16];
-      tmem_ld_32x32b_x32(s_tmem + c0, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const Scales s = sc[c0 / 16 + g];
-        const float ck = s.k * rc, ce = s.log_v - base;
-        float sum = 0.0f;
-#pragma unroll
-        for (int n = 0; n < 16; n += 2) {
-          float x0 = fmaf(__uint_as_float(r[16 * g + n]), ck, ce), x1 = fmaf(__uint_as_float(r[16 * g + n + 1]), ck, ce);
-          if (masked) {
-            if (c0 + 16 * g + n >= vis) x0 = -INFINITY;
-            if (c0 + 16 * g + n + 1 >= vis) x1 = -INFINITY;
-          }
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          sum += x0 + x1;
-          p[8 * g + n / 2] = pack_f16(x0, x1);
-        }
-        l = fmaf(sum, s.inv_v, l);
-      }
-      tmem_st_32x32b_x16(s_tmem + c0 / 2, p);
-    }
+    l += masked ? row_exp<D, true>(s_tmem, sc, rc, base, vis) : row_exp<D, false>(s_tmem, sc, rc, base, vis);
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
@@ -502,6 +702,7 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
     mbar_arrive(&c.join);
     if (!mbar_wait(&c.join, 1)) return;
     l = c.l[0][tid] + c.l[1][tid];
+    m_ref = m;
   }
   // the last products of each stream that adds to this O
   if constexpr (C::kSplitKV) {
@@ -511,7 +712,8 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
     if (!mbar_wait(&c.o_done[w], (n_tiles - 1) & 1)) return;
   }
   tc_fence_after();
-  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  const bool empty = m_ref == -INFINITY && l == l;  // no visible token (a NaN score leaves m_ref, not l)
+  const float f = 1.0f / l;
   constexpr int kCols = C::kSplitKV ? D / 2 : D;
   const int col0 = C::kSplitKV ? w * kCols : 0;
   const int64_t at = (it.sq.start + tok) * a.ld_out + int64_t(head) * D;
@@ -523,7 +725,7 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
     tmem_ld_wait();
 #pragma unroll
     for (int n = 0; n < 32; ++n) {
-      r[n] = __float_as_uint(l == 0.0f ? 0.0f : __uint_as_float(r[n]) * f);
+      r[n] = empty ? 0u : __float_as_uint(__uint_as_float(r[n]) * f);
       if (nan_any && c.nan_first[c0 + n] < lim) r[n] = 0x7fffffffu;
     }
     if (!valid) continue;
@@ -549,7 +751,7 @@ __device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned ch
 
 // Grid: an upper bound of the items; dynamic shared memory smem_bytes<D>().
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_raw[];
   grid_dep_wait();
@@ -570,19 +772,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   }
   const int n_tiles = (it.kv_end + C::BN - 1) / C::BN;
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  unsigned char *qbuf = smem, *kbuf = qbuf + C::Q_BYTES, *vbuf = kbuf + C::STAGES * C::KV_BYTES;
-  Control<D> &c = *reinterpret_cast<Control<D> *>(vbuf + C::STAGES * C::KV_BYTES);
+  unsigned char *qbuf = smem, *kbuf = smem + C::K_OFF, *vbuf = smem + C::V_OFF, *raw = smem + C::RAW_OFF;
+  Control<D> &c = *reinterpret_cast<Control<D> *>(smem + C::CTL_OFF);
   if (tid == 0) {
     mbar_init(&c.q_ready, 256);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.k_full[i], 128);
+      mbar_init(&c.raw_full[i], 1);
+      mbar_init(&c.raw_empty[i], 128);
       mbar_init(&c.v_full[i], 128);
-      mbar_init(&c.k_empty[i], 1);
       mbar_init(&c.v_empty[i], 1);
       mbar_init(&c.s_ready[i], 1);
       mbar_init(&c.p_ready[i], 4);
       mbar_init(&c.o_done[i], 1);
       mbar_init(&c.m_ready[i], 128);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&c.k_full[i], 1);
+      mbar_init(&c.k_empty[i], 1);
     }
     mbar_init(&c.join, 256);
     mbar_init(&c.done, 1);
@@ -590,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     c.nan_any = 0;
   }
   for (int i = tid; i < D; i += kThreads) c.nan_first[i] = 0x7fffffff;
-  if (warp == 16) {
+  if (warp == 12) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
   }
@@ -602,9 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (warp < 8) {
     softmax<D>(a, c, tmem, qbuf, it, n_tiles, warp >> 2, tid & 127);
   } else if (warp < 12) {
-    convert<D, false>(a, c, kbuf, it, n_tiles, tid & 127);
-  } else if (warp < 16) {
-    convert<D, true>(a, c, vbuf, it, n_tiles, tid & 127);
+    convert<D>(a, c, raw, vbuf, it, n_tiles, tid & 127);
+  } else if (warp == 13) {
+    produce<D>(a, &k_map, c, kbuf, raw, it, n_tiles);
   } else if ((tid & 31) == 0) {
     issue<D>(c, tmem, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), n_tiles);
     tc_commit(&c.done);  // whatever was issued has to end before TMEM is given back
@@ -614,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace prompt

@@ -306,7 +306,7 @@ nvfp4_status_t check_batch(const nvfp4_batch_t *b, const nvfp4_block_cache_t *c,
   }
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (b->n_seqs > 65535 || b->tokens > kMaxDim || c->n_kv_heads > 65535 || c->num_blocks > kMaxDim ||
-      b->max_blocks > (kMaxDim >> *log_block) - 1)
+      b->max_blocks > (kMaxDim >> *log_block) - 1 || c->num_blocks * c->n_kv_heads > kMaxDim)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(b->cu_seqlens, 4) || !aligned(b->kv_lens, 4) || !aligned(b->block_table, 4) || !aligned(c->k, 16) ||
       !aligned(c->v, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
@@ -1124,10 +1124,27 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   // Only the device knows the sequences' lengths; no prompt fits in few rows.
   const int64_t rows = batch->tokens * a.group;
   if (rows <= kDecodeRows) return NVFP4_OK;
+  // Tensor map of the K codes as [(block, head)][token][value]: boxes of one head's rows, up to
+  // 128 bytes wide, in the layout of an MMA operand.
+  CUtensorMap k_map;
+  {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return NVFP4_ERR_CUDA;
+    const int D = cache->head_dim, B = cache->block_size, most = D == 256 ? 64 : 128;
+    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(B), cuuint64_t(cache->num_blocks * cache->n_kv_heads)};
+    cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(B) * D};
+    cuuint32_t box[3] = {cuuint32_t(D < 128 ? D : 128), cuuint32_t(B < most ? B : most), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cache->k, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return NVFP4_ERR_CUDA;
+  }
   auto launch_prompt = [&](auto kernel, int tile_rows, int smem) {
     const int64_t items = (rows / tile_rows + batch->n_seqs) * a.kv_heads;
     if (items > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(attn::prompt::kThreads), smem, s, 1, a);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(attn::prompt::kThreads), smem, s, 1, a,
+                      k_map);
   };
   if (i == 0)
     return launch_prompt(attn::prompt::prompt_kernel<64>, attn::prompt::Cfg<64>::ROWS, attn::prompt::smem_bytes<64>());
