@@ -11,18 +11,29 @@
 //  * O += P V runs in FP16, since P needs more than 8 bits of range and precision: a converter
 //    warpgroup turns V codes (exact in FP16) into panels of 64 values with 128-byte swizzle,
 //    token rows, which the product reads as an MN-major operand.
-// S accumulates in TMEM; a softmax warpgroup reads it one row per thread and writes P over it as
-// FP16, the A operand of O += P V.  O stays in TMEM and is rescaled only when a row's maximum has
-// grown by more than 2^kSlack since its reference was set (weights are at most
-// 2^(kSlack + kBoostP), within FP16).
+// S accumulates in TMEM; two softmax warpgroups, one per half of its columns, read it one row per
+// thread and write P over their own half of S as FP16, the A operand of O += P V.  Weights are
+// taken relative to a reference per row, 2^kBoostP at the reference, which stays as it is while the
+// weights fit FP16: a tile costs one pass over S, and the sums of its weights tell whether they did
+// (a sum below FP16's largest value holds none above it).  When one did not (and at the first tile)
+// the warpgroups agree on the rows' maxima, O, which stays in TMEM, is rescaled and the tile's weights
+// are taken again.
 //
 // Two streams keep the tensor cores busy while the other's softmax runs.  Up to 128 values per
 // head they are two tiles of query rows with their own O over the same K / V tiles of 128
-// tokens; at 256 values TMEM holds one O, and the streams are the even and odd K / V tiles of
-// 64 tokens, which hand the rows' reference maxima to each other.
+// tokens; at 256 values TMEM holds one O and four S of 64 tokens, and the streams are the even and odd
+// K / V tiles, which hand the rows' reference maxima to each other.
 //
-// Warps (one CTA per SM): 0-3 and 4-7 softmax of stream 0 and 1, 8-11 V converter, 12 MMA
-// issuer, 13 producer (block table, scales, copies).
+// A product of 128 x 128 x 32 bytes takes 64 cycles and a warp needs about 55 to issue one
+// (measured with descriptors ready in registers; a warp that computes them falls to 75).  At 256
+// values S comes in products of 64 columns, which take half as long: there S and O have an issuer each.
+//
+// Warps (one CTA per SM): 0 and 2 MMA issuers, 1 producer (block table, scales, copies), 3 idle, 4-11
+// and 12-19 softmax of stream 0 and 1 (four warps per half), 20-23 V converter.  Registers are
+// handed from the first and the last warpgroup to the softmax.
+//
+// A wait that runs out sets `ok` to false in the thread that saw it; softmax threads go on through
+// the barriers of their stream without working, so that no one waits for them forever.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -31,9 +42,12 @@ namespace nvfp4 {
 namespace attn {
 namespace prompt {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 768;
+constexpr int kSoftmax = 512;    // softmax threads
+// Registers per thread: 768 threads are launched with 80; 16 * 88 + 4 * 80 + 4 * 48 = 24 * 80.
+constexpr int kRegsSoftmax = 88, kRegsConvert = 80, kRegsOther = 48;
 constexpr int kTile = 128;      // query rows of a tile
-constexpr float kSlack = 8.0f;
+constexpr float kMostSum = 60000.0f;  // weights whose sum is below this are within FP16
 constexpr float kBoostP = 6.0f;
 
 template <int D>
@@ -52,12 +66,19 @@ struct Cfg {
   static constexpr int CPR = D / 16;                   // 16-byte pieces of a row of codes
   static constexpr int PIECES = BN * CPR / 128;        // per converter thread
   static constexpr int ROWS = NQ * kTile;
-  static constexpr int S_COL = BN;                     // TMEM columns of one S
+  static constexpr int SLOTS = kSplitKV ? 4 : 2;       // S buffers: one per stream, or per tile in flight
+  static constexpr int HALF = BN / 2;                  // columns of a softmax warpgroup
   static constexpr int O_COL0 = 256;
   // shared memory: Q, K stages, V (FP16) x 2, V codes x 2
   static constexpr int K_OFF = Q_BYTES, V_OFF = K_OFF + K_STAGES * K_BYTES, RAW_OFF = V_OFF + 2 * V_BYTES,
                        CTL_OFF = RAW_OFF + 2 * K_BYTES;
 };
+
+// S buffer of stream w's tile j, and the parity of the phase that its barriers go through for it.
+template <int D>
+__device__ __forceinline__ int slot(int w, int j) { return Cfg<D>::kSplitKV ? j & 3 : w; }
+template <int D>
+__device__ __forceinline__ uint32_t phase(int j) { return (Cfg<D>::kSplitKV ? j >> 2 : j) & 1; }
 
 struct Scales {
   float k, log_v, inv_v, pad;
@@ -65,8 +86,8 @@ struct Scales {
 
 template <int D>
 struct Control {
-  uint64_t q_ready, k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2], s_ready[2], p_ready[2],
-      o_done[2], m_ready[2], join, done;
+  uint64_t q_ready, k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2],
+      s_ready[4], p_ready[4], o_done[4], m_ready[2], join, done;  // s_ready, p_ready, o_done: by S buffer
   uint32_t tmem;
   int nan_any;
   // Scales and the mask of the groups that hold tokens, by tile.  A slot comes up again eight
@@ -75,8 +96,10 @@ struct Control {
   Scales ks[8][Cfg<D>::GROUPS];
   uint32_t valid[8];
   int nan_first[D];
-  float m_ref[kTile];            // kSplitKV: reference maxima of the rows
-  float l[2][kTile];
+  float rc[Cfg<D>::ROWS];        // score scale of each query row, times log2(e)
+  float mx[2][2][kTile];         // by stream and half: maximum of a row's half
+  float m_ref[2][kTile];         // kSplitKV: reference maxima of the rows, by parity of the tile
+  float l[4][kTile];
 };
 
 template <int D>
@@ -88,22 +111,48 @@ __host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool b_mn_major)
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
-// FP8 MMA, both operands E4M3 in shared memory, and FP16 MMA with A in TMEM; FP32 accumulation.
-// (The E4M3 codes of the descriptor's type fields are 0, as are FP16's.)
-__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// 1 in one lane of the warp.  elect.sync and not a comparison of lane numbers: the compiler then
+// knows that one lane issues and spends fewer instructions on each product (8192-token prompt
+// 1073 -> 940 us).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
+// FP8 MMA, both operands E4M3 in shared memory, and FP16 MMA with A in TMEM; FP32 accumulation.
+// (The E4M3 codes of the descriptor's type fields are 0, as are FP16's.)  Called by whole
+// warps, so that operands stay warp-uniform; the lane with `elected` != 0 issues.
+__device__ __forceinline__ void mma_f8_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(elected)
       : "memory");
 }
 
@@ -342,98 +391,124 @@ __device__ void convert(const Args &a, Control<D> &c, const unsigned char *raw, 
 #pragma unroll
     for (int i = 0; i < C::PIECES; ++i) {
       const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint4 h[2];
-      h[0] = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]), e4m3x2_to_f16x2(w[1] >> 16));
-      h[1] = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]), e4m3x2_to_f16x2(w[3] >> 16));
-      // the odd piece first in every other panel: eight lanes then hit distinct banks
+      // every other panel stores its odd piece first: eight lanes then hit distinct banks
       const int o = (col >> 2) & 1;
-      *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + o)) = o ? h[1] : h[0];
-      *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + (o ^ 1))) = o ? h[0] : h[1];
+      const uint2 first = o ? make_uint2(x[i].z, x[i].w) : make_uint2(x[i].x, x[i].y);
+      const uint2 second = o ? make_uint2(x[i].x, x[i].y) : make_uint2(x[i].z, x[i].w);
+      auto half = [](uint2 w) {
+        return make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+      };
+      *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + o)) = half(first);
+      *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + (o ^ 1))) = half(second);
     }
     fence_async_smem();
     mbar_arrive(&c.v_full[st]);
   }
 }
 
-// MMA issuer (one thread).
+// MMA issuers (whole warps).  All 512 TMEM columns are this CTA's: addresses start at 0.
+// Descriptors are built once; within an operand they differ in the address field.
 template <int D>
-__device__ void issue(Control<D> &c, uint32_t tmem, uint32_t q, uint32_t k, uint32_t v, int n_tiles) {
+struct Issuer {
   using C = Cfg<D>;
-  constexpr uint32_t kIdescS = make_idesc(kTile, C::BN, false), kIdescO = make_idesc(kTile, D, true);
-  auto desc = [](uint32_t at) { return D < 128 ? sdesc_sw64_kmajor(at) : sdesc_sw128_kmajor(at); };
-  auto qk = [&](int w, int j) {  // stream w's S = (hi + lo) K_j^T
-    const uint32_t qa = q + (C::kSplitKV ? 0 : w * 2 * C::Q_PART), ka = k + (j % C::K_STAGES) * C::K_BYTES;
+  static constexpr uint32_t kIdescS = make_idesc(kTile, C::BN, false), kIdescO = make_idesc(kTile, D, true);
+  Control<D> &c;
+  uint32_t elected;
+  uint64_t qd, kd, vd;
+
+  __device__ Issuer(Control<D> &c, uint32_t q, uint32_t k, uint32_t v) : c(c), elected(elect_one()) {
+    qd = D < 128 ? sdesc_sw64_kmajor(q) : sdesc_sw128_kmajor(q);
+    kd = D < 128 ? sdesc_sw64_kmajor(k) : sdesc_sw128_kmajor(k);
+    vd = sdesc_sw128_mnmajor(v, C::BN * 128);
+  }
+
+  // S = (hi + lo) K_j^T of stream w
+  __device__ __forceinline__ void qk(int w, int j) const {
+    const uint64_t a = qd + (C::kSplitKV ? 0 : w * (2 * C::Q_PART >> 4)), b = kd + (j % C::K_STAGES) * (C::K_BYTES >> 4);
+    const uint32_t s_col = slot<D>(w, j) * C::BN;
 #pragma unroll
     for (int part = 0; part < 2; ++part)
 #pragma unroll
-      for (int p = 0; p < C::PANELS8; ++p) {
-        const uint64_t ad = desc(qa + part * C::Q_PART + p * kTile * 128), bd = desc(ka + p * C::BN * 128);
+      for (int p = 0; p < C::PANELS8; ++p)
 #pragma unroll
         for (int s = 0; s < C::ROWB / 32; ++s)
-          mma_f8_ss(tmem + w * C::S_COL, ad + 2 * s, bd + 2 * s, kIdescS, (part | p | s) != 0);
-      }
-    tc_commit(&c.s_ready[w]);
-  };
-  auto pv = [&](int w, int j) {  // O += P V_j
-    const uint32_t va = v + (j & 1) * C::V_BYTES;
-    const uint32_t o = tmem + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
+          mma_f8_ss(elected, s_col, a + (part * C::Q_PART + p * kTile * 128 + 32 * s) / 16, b + (p * C::BN * 128 + 32 * s) / 16,
+                    kIdescS, (part | p | s) != 0);
+    commit(elected, &c.s_ready[slot<D>(w, j)]);
+  }
+  // O += P V_j
+  __device__ __forceinline__ void pv(int w, int j) const {
+    const uint64_t b = vd + (j & 1) * (C::V_BYTES >> 4);
+    const uint32_t p_col = slot<D>(w, j) * C::BN, o_col = C::O_COL0 + (C::kSplitKV ? 0 : w * D);
+    constexpr int H = C::HALF / 16;  // k-steps of a half row
 #pragma unroll
-    for (int s = 0; s < C::BN / 16; ++s)
-      mma_f16_ts(o, tmem + w * C::S_COL + 8 * s, sdesc_sw128_mnmajor(va + s * 2048, C::BN * 128), kIdescO, (j | s) != 0);
-    tc_commit(&c.o_done[w]);
-  };
-  auto k_full = [&](int j) { return mbar_wait(&c.k_full[j % C::K_STAGES], (j / C::K_STAGES) & 1); };
-  auto k_done = [&](int j) { tc_commit(&c.k_empty[j % C::K_STAGES]); };
-  auto v_full = [&](int j) { return mbar_wait(&c.v_full[j & 1], (j >> 1) & 1); };
-
-  if (!mbar_wait(&c.q_ready, 0)) return;
-  if constexpr (!C::kSplitKV) {
-    if (!k_full(0)) return;
+    for (int s = 0; s < 2 * H; ++s)
+      mma_f16_ts(elected, o_col, p_col + (s / H) * C::HALF + 8 * (s % H), b + s * (2048 / 16), kIdescO, (j | s) != 0);
+    commit(elected, &c.o_done[slot<D>(w, j)]);
+  }
+  __device__ __forceinline__ bool k_full(int j) const {
+    const bool ok = mbar_wait(&c.k_full[j % C::K_STAGES], (j / C::K_STAGES) & 1);
     tc_fence_after();
-    qk(0, 0);
-    qk(1, 0);
-    k_done(0);
+    return __all_sync(0xffffffffu, ok);
+  }
+  __device__ __forceinline__ bool p_ready(int w, int j) const {
+    const bool ok = mbar_wait(&c.v_full[j & 1], (j >> 1) & 1) && mbar_wait(&c.p_ready[slot<D>(w, j)], phase<D>(j));
+    tc_fence_after();
+    return __all_sync(0xffffffffu, ok);
+  }
+  __device__ __forceinline__ void k_done(int j) const { commit(elected, &c.k_empty[j % C::K_STAGES]); }
+  __device__ __forceinline__ void v_done(int j) const { commit(elected, &c.v_empty[j & 1]); }
+
+  // Issuer w of two.
+  __device__ void run(int w, int n_tiles) const {
+    if (!__all_sync(0xffffffffu, mbar_wait(&c.q_ready, 0))) return;
+    if constexpr (!C::kSplitKV) {
+      // Both streams in turn: each gets its products in one piece, which keeps the streams half a
+      // period apart (with an issuer each they fell into step, and the tensor cores idled while
+      // both took exponentials: 5040 cycles per tile against 4290).
+      if (w == 1) return;
+      if (!k_full(0)) return;
+      qk(0, 0);
+      qk(1, 0);
+      k_done(0);
 #pragma unroll 1
-    for (int j = 0; j < n_tiles; ++j) {
-      if (!v_full(j)) return;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (!mbar_wait(&c.p_ready[w], j & 1)) return;
-        tc_fence_after();
-        pv(w, j);
-        if (w == 1) tc_commit(&c.v_empty[j & 1]);
+      for (int j = 0; j < n_tiles; ++j) {
+        if (!p_ready(0, j)) return;
+        pv(0, j);
         if (j + 1 < n_tiles) {
-          if (w == 0 && !k_full(j + 1)) return;
-          tc_fence_after();
-          qk(w, j + 1);
-          if (w == 1) k_done(j + 1);
+          if (!k_full(j + 1)) return;
+          qk(0, j + 1);  // over P_j: products of one issuer run in order
+        }
+        if (!p_ready(1, j)) return;
+        pv(1, j);
+        v_done(j);
+        if (j + 1 < n_tiles) {
+          qk(1, j + 1);
+          k_done(j + 1);
         }
       }
-    }
-  } else {
-    for (int j = 0; j < 2 && j < n_tiles; ++j) {
-      if (!k_full(j)) return;
-      tc_fence_after();
-      qk(j, j);
-      k_done(j);
-    }
+    } else if (w == 0) {  // S, up to four tiles ahead of O
 #pragma unroll 1
-    for (int j = 0; j < n_tiles; ++j) {
-      const int w = j & 1;
-      if (!v_full(j) || !mbar_wait(&c.p_ready[w], (j >> 1) & 1)) return;
-      tc_fence_after();
-      pv(w, j);
-      tc_commit(&c.v_empty[w]);
-      if (j + 2 < n_tiles) {
-        if (!k_full(j + 2)) return;
-        tc_fence_after();
-        qk(w, j + 2);
-        k_done(j + 2);
+      for (int j = 0; j < n_tiles; ++j) {
+        if (!k_full(j)) return;
+        if (j >= 4) {  // the buffer held P_{j-4}
+          const bool ok = mbar_wait(&c.o_done[j & 3], phase<D>(j - 4));
+          tc_fence_after();
+          if (!__all_sync(0xffffffffu, ok)) return;
+        }
+        qk(0, j);
+        k_done(j);
+      }
+    } else {  // O
+#pragma unroll 1
+      for (int j = 0; j < n_tiles; ++j) {
+        if (!p_ready(0, j)) return;
+        pv(0, j);
+        v_done(j);
       }
     }
   }
-}
+};
 
 // Multiplies columns [0, n) of the thread's O row by f.
 template <int N>
@@ -473,38 +548,16 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
   return r;
 }
 
-// 2^x for two values on the FMA pipe: 2^n 2^f with n = round(x), f in [-1/2, 1/2], and a
-// polynomial of degree 4 for 2^f (minimax in relative error by Remez' exchange, 2^-18.5, far
-// below the FP16 rounding that follows).  x >= -126 after clamping; not for NaN.
-__device__ __forceinline__ float2 exp2_poly(float2 x) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves round(x) in the low bits
-  x.x = fmaxf(x.x, -126.0f);
-  x.y = fmaxf(x.y, -126.0f);
-  const float2 t = add_f32x2(x, make_float2(kMagic, kMagic));
-  const float2 n = add_f32x2(t, make_float2(-kMagic, -kMagic));
-  const float2 f = fma_f32x2(n, make_float2(-1.0f, -1.0f), x);
-  float2 p = fma_f32x2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
-                       make_float2(0.05591785907745361f, 0.05591785907745361f));
-  p = fma_f32x2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  p = fma_f32x2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  p = fma_f32x2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-
-// Maximum of x = s c + e over the thread's row of S, NaN if there is one; MASK: only the first `vis` columns.
+// Maximum of x = s c + e over the thread's half row of S, NaN if there is one; MASK: only the
+// first `vis` columns.
 template <int D, bool MASK>
 __device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, float rc, int vis) {
-  using C = Cfg<D>;
-  constexpr int N = C::BN / 32;
   float mt = -INFINITY;
-  uint32_t r[2][32];
-  tmem_ld_32x32b_x32(s_tmem, r[0]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t(&v)[32] = r[i & 1];
+  for (int i = 0; i < Cfg<D>::HALF / 32; ++i) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(s_tmem + 32 * i, v);
     tmem_ld_wait();
-    if (i + 1 < N) tmem_ld_32x32b_x32(s_tmem + 32 * (i + 1), r[(i + 1) & 1]);
     if constexpr (MASK) {
 #pragma unroll
       for (int n = 0; n < 32; ++n)
@@ -530,20 +583,18 @@ __device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, floa
   return mt;
 }
 
-// P = 2^(x - base) over S, as FP16; returns sum of P / sV.
+// P = 2^(x - base) over the half row of S as FP16 in p, sum of P / sV in l; returns the sum of
+// P (NaN if a score is).  MASK: only the first `vis` columns.
 template <int D, bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, float rc, float base, int vis) {
-  using C = Cfg<D>;
-  constexpr int N = C::BN / 32;
-  float l = 0.0f;
-  uint32_t r[2][32];
-  tmem_ld_32x32b_x32(s_tmem, r[0]);
+__device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, float rc, float base, int vis,
+                                         uint32_t (&p)[Cfg<D>::HALF / 2], float &l) {
+  float all = 0.0f;
+  l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t(&v)[32] = r[i & 1];
+  for (int i = 0; i < Cfg<D>::HALF / 32; ++i) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(s_tmem + 32 * i, v);
     tmem_ld_wait();
-    if (i + 1 < N) tmem_ld_32x32b_x32(s_tmem + 32 * (i + 1), r[(i + 1) & 1]);
-    uint32_t p[16];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const Scales s = sc[2 * i + g];
@@ -557,165 +608,218 @@ __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, floa
           if (32 * i + 16 * g + n >= vis) x.x = -INFINITY;
           if (32 * i + 16 * g + n + 1 >= vis) x.y = -INFINITY;
         }
-        // one pair in four on the FMA pipe: the MUFU's 16 exponentials per clock are the bound
-        if (n % 8 == 6) {
-          x = exp2_poly(x);
-        } else {
-          x.x = ex2(x.x);
-          x.y = ex2(x.y);
-        }
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
         sum = add_f32x2(sum, x);
-        p[8 * g + n / 2] = pack_f16(x.x, x.y);
+        p[16 * i + 8 * g + n / 2] = pack_f16(x.x, x.y);
       }
+      all += sum.x + sum.y;
       l = fmaf(sum.x + sum.y, s.inv_v, l);
     }
-    tmem_st_32x32b_x16(s_tmem + 16 * i, p);
   }
-  return l;
+  return all;
 }
 
-// Softmax warpgroup of stream w; tid 0..127 is the row of its tile.
+template <int N>
+__device__ __forceinline__ void store_p(uint32_t s_tmem, const uint32_t (&p)[N]) {
+  static_assert(N == 16 || N == 32, "");
+  if constexpr (N == 16) tmem_st_32x32b_x16(s_tmem, p);
+  else tmem_st_32x32b_x32(s_tmem, p);
+}
+
+// Barrier of the 256 softmax threads of stream w; true if `any` was true in one of them.
+__device__ __forceinline__ bool stream_any(int w, bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(w + 1), "r"(static_cast<uint32_t>(any))
+      : "memory");
+  return r != 0;
+}
+
+// The CTA's query rows in two E4M3 parts, scaled by 2^-e; a warp takes whole rows.
 template <int D>
-__device__ void softmax(const Args &a, Control<D> &c, uint32_t tmem, unsigned char *qbuf, const Item &it, int n_tiles,
-                        int w, int tid) {
+__device__ void load_queries(const Args &a, Control<D> &c, unsigned char *qbuf, const Item &it, int warp) {
+  using C = Cfg<D>;
+  constexpr int N = D / 32;  // values per lane
+  constexpr int kDepth = 4;  // rows in flight
+  const int lane = threadIdx.x & 31, n_rows = it.sq.q_len * a.group;
+  constexpr int kPer = C::ROWS / (kSoftmax / 32);
+  const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+#pragma unroll 1
+  for (int r0 = warp * kPer; r0 < (warp + 1) * kPer; r0 += kDepth) {
+    uint32_t raw[kDepth][N / 2];
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      const int R = it.row0 + r0 + u;
+      const bool ok = R < n_rows;
+      const uint16_t *src = a.q + (it.sq.start + (ok ? R / a.group : 0)) * a.ld_q + int64_t(it.h * a.group + (ok ? R % a.group : 0)) * D + lane * N;
+      if constexpr (N == 8) {
+        const uint4 x = ok ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+        raw[u][0] = x.x, raw[u][1] = x.y, raw[u][2] = x.z, raw[u][3] = x.w;
+      } else if constexpr (N == 4) {
+        const uint2 x = ok ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
+        raw[u][0] = x.x, raw[u][1] = x.y;
+      } else {
+        raw[u][0] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N / 2; ++n)
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[u][n] << 16)), fabsf(__uint_as_float(raw[u][n] & 0xFFFF0000u))));
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // magnitudes order as integers
+      // 2^-e brings the largest magnitude into (224, 448], 448 = 1.75 * 2^8
+      const uint32_t bits = __float_as_uint(amax);
+      const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+      // an infinite value makes every score of the row infinite or NaN: the row is NaN
+      const float f = bits < 0x7f800000u ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * sign : __int_as_float(0x7fffffff);
+      const int r = r0 + u, row = r & (kTile - 1);
+      if (lane == 0) c.rc[r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(min(e, 120) + 127) << 23);
+      uint16_t hi[N / 2], lo[N / 2];
+#pragma unroll
+      for (int n = 0; n < N / 2; ++n) {
+        const float x0 = __uint_as_float(raw[u][n] << 16) * f, x1 = __uint_as_float(raw[u][n] & 0xFFFF0000u) * f;
+        hi[n] = cvt_e4m3x2(x1, x0);
+        const uint32_t back = e4m3x2_to_f16x2(hi[n]);
+        const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+        lo[n] = cvt_e4m3x2(x1 - hf.y, x0 - hf.x);
+      }
+      unsigned char *dst = qbuf + (r / kTile) * 2 * C::Q_PART + code_offset<D>(kTile, row, lane * N / 16) + (lane * N) % 16;
+      if constexpr (N == 8) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0] | uint32_t(hi[1]) << 16, hi[2] | uint32_t(hi[3]) << 16);
+        *reinterpret_cast<uint2 *>(dst + C::Q_PART) = make_uint2(lo[0] | uint32_t(lo[1]) << 16, lo[2] | uint32_t(lo[3]) << 16);
+      } else if constexpr (N == 4) {
+        *reinterpret_cast<uint32_t *>(dst) = hi[0] | uint32_t(hi[1]) << 16;
+        *reinterpret_cast<uint32_t *>(dst + C::Q_PART) = lo[0] | uint32_t(lo[1]) << 16;
+      } else {
+        *reinterpret_cast<uint16_t *>(dst) = hi[0];
+        *reinterpret_cast<uint16_t *>(dst + C::Q_PART) = lo[0];
+      }
+    }
+  }
+  fence_async_smem();
+  mbar_arrive(&c.q_ready);
+}
+
+// Softmax warpgroup of half `hf` of stream w; tid 0..127 is the row of its tile.
+template <int D>
+__device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tiles, int w, int hf, int tid) {
   using C = Cfg<D>;
   const int n_rows = it.sq.q_len * a.group;
-  const int R = it.row0 + (C::kSplitKV ? 0 : w * kTile) + tid;
+  const int local = (C::kSplitKV ? 0 : w * kTile) + tid, R = it.row0 + local;
   const bool valid = R < n_rows;
   const int tok = valid ? R / a.group : 0, head = it.h * a.group + (valid ? R % a.group : 0);
   const int lim = !valid ? it.kv_end : a.causal ? it.sq.kv_len - it.sq.q_len + tok + 1 : it.sq.kv_len;
   const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
-
-  // This thread's Q row in two E4M3 parts, scaled by 2^-e (both streams of kSplitKV need e; each
-  // writes half of the row).
-  float rc;
-  {
-    const uint16_t *src = a.q + (it.sq.start + tok) * a.ld_q + int64_t(head) * D;
-    float amax = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-      const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[n] << 16)), fabsf(__uint_as_float(v[n] & 0xFFFF0000u))));
-    }
-    const int e = row_exponent(amax) + 6;  // largest magnitude in [2^8, 2^9); see below
-    // magnitudes above 448 = 1.75 * 2^8 take one more halving
-    const int ee = amax > 448.0f * ldexpf(1.0f, min(e, 118)) && amax <= 3.4e38f ? e + 1 : e;
-    // an infinite value makes every score of the row infinite or NaN: the row is NaN
-    const float f0 = !valid ? 0.0f : amax <= 3.4e38f ? ldexpf(a.scale_log2 < 0.0f ? -1.0f : 1.0f, -(ee / 2)) : __int_as_float(0x7fffffff);
-    const float f1 = ldexpf(1.0f, -(ee - ee / 2));
-    rc = ldexpf(fabsf(a.scale_log2), ee);
-    unsigned char *hi = qbuf + (C::kSplitKV ? 0 : w * 2 * C::Q_PART), *lo = hi + C::Q_PART;
-    constexpr int kPieces = C::kSplitKV ? D / 32 : D / 16;
-    const int first = C::kSplitKV ? w * kPieces : 0;
-#pragma unroll 2
-    for (int i = first; i < first + kPieces; ++i) {  // 16 values
-      uint32_t oh[4], ol[4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 x = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + 2 * i + k) : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int n = 0; n < 4; n += 2) {
-          uint32_t h = 0, l8 = 0;
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const float x0 = __uint_as_float(v[n + m] << 16) * f0 * f1, x1 = __uint_as_float(v[n + m] & 0xFFFF0000u) * f0 * f1;
-            const uint32_t c8 = cvt_e4m3x2(x1, x0);
-            const uint32_t back = e4m3x2_to_f16x2(c8);
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-            h |= c8 << (16 * m);
-            l8 |= static_cast<uint32_t>(cvt_e4m3x2(x1 - hf.y, x0 - hf.x)) << (16 * m);
-          }
-          oh[2 * k + n / 2] = h;
-          ol[2 * k + n / 2] = l8;
-        }
-      }
-      *reinterpret_cast<uint4 *>(hi + code_offset<D>(kTile, tid, i)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-      *reinterpret_cast<uint4 *>(lo + code_offset<D>(kTile, tid, i)) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-    }
-    fence_async_smem();
-    mbar_arrive(&c.q_ready);
-  }
+  bool ok = mbar_wait(&c.q_ready, 0);
+  const float rc = c.rc[local];
 
   const uint32_t lanes = (tid & ~31) << 16;  // TMEM lane quadrant of the warp
-  const uint32_t s_tmem = tmem + lanes + w * C::S_COL, o_tmem = tmem + lanes + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
+  const uint32_t o_tmem = lanes + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
   float m_ref = -INFINITY, l = 0.0f;
   const int steps = C::kSplitKV ? (n_tiles - w + 1) / 2 : n_tiles;
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     const int j = C::kSplitKV ? 2 * i + w : i;
-    if (!mbar_wait(&c.s_ready[w], i & 1)) return;
+    const int sl = slot<D>(w, j);
+    const uint32_t s_tmem = lanes + sl * C::BN + hf * C::HALF;
+    ok = ok && mbar_wait(&c.s_ready[sl], phase<D>(j));
+    ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    const Scales *sc = c.ks[j & 7];
-    const int vis = lim - j * C::BN;  // visible columns of this row
-    const bool masked = warp_lim < (j + 1) * C::BN;
-
-    const float mt = masked ? row_max<D, true>(s_tmem, sc, rc, vis) : row_max<D, false>(s_tmem, sc, rc, vis);
-
-    if constexpr (C::kSplitKV) {
-      if (j > 0) {
-        if (!mbar_wait(&c.m_ready[w ^ 1], w == 1 ? i & 1 : (i - 1) & 1)) return;
-        const float m = c.m_ref[tid];
-        if (m != m_ref) l *= m_ref == -INFINITY ? 0.0f : ex2(m_ref - m);
-        m_ref = m;
+    const Scales *sc = c.ks[j & 7] + hf * (C::GROUPS / 2);
+    const int col0 = j * C::BN + hf * C::HALF;
+    const int vis = lim - col0;  // visible columns of this half row
+    const bool masked = warp_lim < col0 + C::HALF;
+    uint32_t p[C::HALF / 2];
+    float add = 0.0f;
+    // The reference that the other stream's tile j - 1 left (kSplitKV).
+    auto follow = [&] {
+      ok = ok && mbar_wait(&c.m_ready[w ^ 1], w == 1 ? i & 1 : (i - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      const float m = c.m_ref[(j - 1) & 1][tid];
+      const bool moved = m != m_ref;
+      if (moved) l *= m_ref == -INFINITY ? 0.0f : ex2(m_ref - m);
+      m_ref = m;
+      return __any_sync(0xffffffffu, moved);
+    };
+    if (C::kSplitKV && j == 1) follow();
+    bool over = j == 0;  // no reference yet: straight to the maxima
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 1 || !over) {
+        float all = 0.0f;
+        if (ok) {
+          const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kBoostP;
+          all = masked ? row_exp<D, true>(s_tmem, sc, rc, base, vis, p, add) : row_exp<D, false>(s_tmem, sc, rc, base, vis, p, add);
+        }
+        if (pass == 1) break;
+        over = stream_any(w, !(all < kMostSum) || (m_ref == -INFINITY && all > 0.0f));
       }
+      bool moved = false;
+      if (C::kSplitKV && j > 1) moved = follow();
+      if (over) {
+        float mt = -INFINITY;
+        if (ok) mt = masked ? row_max<D, true>(s_tmem, sc, rc, vis) : row_max<D, false>(s_tmem, sc, rc, vis);
+        c.mx[w][hf][tid] = mt;
+        stream_any(w, false);
+        mt = fmaxf_nan(mt, c.mx[w][hf ^ 1][tid]);
+        if (!(mt < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or infinite score: so is the row
+        const bool grow = mt > m_ref;
+        const float f = grow ? ex2(m_ref - mt) : 1.0f;
+        if (grow) {
+          l *= f;
+          m_ref = mt;
+        }
+        if (j > 0) {  // O holds the earlier tiles: it may be touched once their products are in
+          ok = ok && mbar_wait(&c.o_done[slot<D>(w, j - 1)], phase<D>(j - 1));
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          if (ok && __any_sync(0xffffffffu, grow)) scale_o<D / 2>(o_tmem + hf * (D / 2), f);
+        }
+      }
+      if (!over && !moved) break;
     }
-    if (!(mt < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or infinite score: so is the row
-    const bool grow = mt > m_ref + kSlack || (m_ref == -INFINITY && mt > m_ref);
-    if (__any_sync(0xffffffffu, grow)) {
-      const float f = grow ? ex2(m_ref - mt) : 1.0f;
-      if (grow) {
-        l *= f;
-        m_ref = mt;
-      }
-      if (j > 0) {  // O holds the earlier tiles: it may be touched once their products are in
-        // S_j was issued after the products of this stream's previous tile, so only the
-        // latest phase can be open
-        if (!mbar_wait(&c.o_done[C::kSplitKV ? w ^ 1 : w], (C::kSplitKV ? (j - 1) >> 1 : j - 1) & 1)) return;
-        tc_fence_after();
-        scale_o<D>(o_tmem, f);
-      }
-    }
+    l += add;
     if constexpr (C::kSplitKV) {
-      c.m_ref[tid] = m_ref;
+      if (hf == 0) c.m_ref[j & 1][tid] = m_ref;  // read last for tile j - 1, whose both halves arrived
       mbar_arrive(&c.m_ready[w]);
     }
-
-    const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kBoostP;
-    l += masked ? row_exp<D, true>(s_tmem, sc, rc, base, vis) : row_exp<D, false>(s_tmem, sc, rc, base, vis);
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(&c.p_ready[w]);
+    if (ok) {
+      store_p(s_tmem, p);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(&c.p_ready[sl]);
+    }
   }
 
-  // Epilogue: O / l.
+  // Join the partial sums, then O / l.
   if constexpr (C::kSplitKV) {
     mbar_arrive(&c.join);
-    if (!mbar_wait(&c.join, 0)) return;
-    const float m = c.m_ref[tid];  // the last tile's reference; l is relative to the one seen last
+    ok = ok && mbar_wait(&c.join, 0);
+    const float m = c.m_ref[(n_tiles - 1) & 1][tid];  // the last reference; l is relative to the one seen last
     if (m != m_ref && m_ref != -INFINITY) l *= ex2(m_ref - m);
-    c.l[w][tid] = l;
-    mbar_arrive(&c.join);
-    if (!mbar_wait(&c.join, 1)) return;
-    l = c.l[0][tid] + c.l[1][tid];
     m_ref = m;
   }
-  // the last products of each stream that adds to this O
-  if constexpr (C::kSplitKV) {
-    if (!mbar_wait(&c.o_done[0], ((n_tiles - 1) >> 1) & 1)) return;
-    if (n_tiles > 1 && !mbar_wait(&c.o_done[1], ((n_tiles >> 1) - 1) & 1)) return;
-  } else {
-    if (!mbar_wait(&c.o_done[w], (n_tiles - 1) & 1)) return;
-  }
+  c.l[2 * w + hf][tid] = l;
+  mbar_arrive(&c.join);
+  ok = ok && mbar_wait(&c.join, C::kSplitKV ? 1 : 0);
+  l = c.l[2 * w][tid] + c.l[2 * w + 1][tid];
+  if constexpr (C::kSplitKV) l += c.l[2 * (w ^ 1)][tid] + c.l[2 * (w ^ 1) + 1][tid];
+  ok = ok && mbar_wait(&c.o_done[slot<D>(w, n_tiles - 1)], phase<D>(n_tiles - 1));  // the last products, and all before
+  if (!__all_sync(0xffffffffu, ok)) return;
   tc_fence_after();
   const bool empty = m_ref == -INFINITY && l == l;  // no visible token (a NaN score leaves m_ref, not l)
   const float f = 1.0f / l;
-  constexpr int kCols = C::kSplitKV ? D / 2 : D;
-  const int col0 = C::kSplitKV ? w * kCols : 0;
+  constexpr int kCols = C::kSplitKV ? D / 4 : D / 2;
+  const int col0 = (C::kSplitKV ? 2 * w + hf : hf) * kCols;
   const int64_t at = (it.sq.start + tok) * a.ld_out + int64_t(head) * D;
   const bool nan_any = *const_cast<volatile int *>(&c.nan_any) != 0;
 #pragma unroll 1
@@ -758,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   grid_dep_launch();
   Item it;
   if (!find_item<D>(a, it)) return;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (it.kv_end == 0) {  // no row sees a token
     const int n_rows = it.sq.q_len * a.group;
     for (int r = it.row0 + warp; r < min(it.row0 + C::ROWS, n_rows); r += kThreads / 32) {
@@ -775,52 +879,60 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   unsigned char *qbuf = smem, *kbuf = smem + C::K_OFF, *vbuf = smem + C::V_OFF, *raw = smem + C::RAW_OFF;
   Control<D> &c = *reinterpret_cast<Control<D> *>(smem + C::CTL_OFF);
   if (tid == 0) {
-    mbar_init(&c.q_ready, 256);
+    mbar_init(&c.q_ready, kSoftmax);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.raw_full[i], 1);
       mbar_init(&c.raw_empty[i], 128);
       mbar_init(&c.v_full[i], 128);
       mbar_init(&c.v_empty[i], 1);
-      mbar_init(&c.s_ready[i], 1);
-      mbar_init(&c.p_ready[i], 4);
-      mbar_init(&c.o_done[i], 1);
-      mbar_init(&c.m_ready[i], 128);
+      mbar_init(&c.m_ready[i], 256);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&c.k_full[i], 1);
       mbar_init(&c.k_empty[i], 1);
     }
-    mbar_init(&c.join, 256);
-    mbar_init(&c.done, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&c.s_ready[i], 1);
+      mbar_init(&c.p_ready[i], 8);
+      mbar_init(&c.o_done[i], 1);
+    }
+    mbar_init(&c.join, kSoftmax);
+    mbar_init(&c.done, 2);
     fence_barrier_init();
     c.nan_any = 0;
   }
   for (int i = tid; i < D; i += kThreads) c.nan_first[i] = 0x7fffffff;
-  if (warp == 12) {
+  if (warp == 0) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = c.tmem;
 
-  if (warp < 8) {
-    softmax<D>(a, c, tmem, qbuf, it, n_tiles, warp >> 2, tid & 127);
-  } else if (warp < 12) {
+  if (warp >= 20) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
     convert<D>(a, c, raw, vbuf, it, n_tiles, tid & 127);
-  } else if (warp == 13) {
-    produce<D>(a, &k_map, c, kbuf, raw, it, n_tiles);
-  } else if ((tid & 31) == 0) {
-    issue<D>(c, tmem, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), n_tiles);
-    tc_commit(&c.done);  // whatever was issued has to end before TMEM is given back
-    mbar_wait(&c.done, 0);
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    load_queries<D>(a, c, qbuf, it, warp - 4);
+    softmax<D>(a, c, it, n_tiles, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, tid & 127);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 1) {
+      produce<D>(a, &k_map, c, kbuf, raw, it, n_tiles);
+    } else if (warp != 3) {
+      Issuer<D> mma(c, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf));
+      mma.run(warp >> 1, __reduce_max_sync(0xffffffffu, n_tiles));  // uniform for the compiler too
+      commit(mma.elected, &c.done);  // whatever was issued has to end before TMEM is given back
+      mbar_wait(&c.done, 0);
+    }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(c.tmem, 512);
 }
 
 }  // namespace prompt
