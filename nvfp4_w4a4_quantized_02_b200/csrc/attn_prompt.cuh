@@ -87,7 +87,7 @@ struct Scales {
 template <int D>
 struct Control {
   uint64_t q_ready, k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2],
-      s_ready[4], p_ready[4], o_done[4], m_ready[2], join, done;  // s_ready, p_ready, o_done: by S buffer
+      s_ready[4], p_ready[4], o_done[4], m_ready[2], join, done[2];  // s_ready, p_ready, o_done: by S buffer
   uint32_t tmem;
   int nan_any;
   // Scales and the mask of the groups that hold tokens, by tile.  A slot comes up again eight
@@ -211,6 +211,12 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 // Generic-proxy writes to shared memory become visible to the tensor cores.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One arrival for the warp, after what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 // 16-byte piece `c` (of 8) of row `r` of panel `p`, a panel holding `rows` rows.
 __device__ __forceinline__ uint32_t panel_offset(int rows, int p, int r, int c) {
@@ -364,7 +370,7 @@ __device__ void convert(const Args &a, Control<D> &c, const unsigned char *raw, 
 #pragma unroll
     for (int i = 0; i < C::PIECES; ++i)
       x[i] = *reinterpret_cast<const uint4 *>(raw + st * C::K_BYTES + (tid + 128 * i) * 16);
-    mbar_arrive(&c.raw_empty[st]);
+    warp_arrive(&c.raw_empty[st]);
     if (have != all || (j + 1) * C::BN > it.lim_min) {
 #pragma unroll
       for (int i = 0; i < C::PIECES; ++i) {
@@ -548,6 +554,26 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
   return r;
 }
 
+// 2^x for two values on the FMA pipe: 2^n 2^f with n = round(x), f in [-1/2, 1/2], and a
+// polynomial of degree 4 for 2^f (minimax in relative error by Remez' exchange, 2^-18.5, far
+// below the FP16 rounding that follows).  x is clamped to [-126, 127]; a NaN becomes 2^127, which
+// the check of the weights' sum catches.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves round(x) in the low bits
+  x.x = fminf(fmaxf_nan(x.x, -126.0f), 127.0f);
+  x.y = fminf(fmaxf_nan(x.y, -126.0f), 127.0f);
+  const float2 t = add_f32x2(x, make_float2(kMagic, kMagic));
+  const float2 n = add_f32x2(t, make_float2(-kMagic, -kMagic));
+  const float2 f = fma_f32x2(n, make_float2(-1.0f, -1.0f), x);
+  float2 p = fma_f32x2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+                       make_float2(0.05591785907745361f, 0.05591785907745361f));
+  p = fma_f32x2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  p = fma_f32x2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  p = fma_f32x2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
 // Maximum of x = s c + e over the thread's half row of S, NaN if there is one; MASK: only the
 // first `vis` columns.
 template <int D, bool MASK>
@@ -608,8 +634,15 @@ __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, floa
           if (32 * i + 16 * g + n >= vis) x.x = -INFINITY;
           if (32 * i + 16 * g + n + 1 >= vis) x.y = -INFINITY;
         }
-        x.x = ex2(x.x);
-        x.y = ex2(x.y);
+        // The MUFU's 16 exponentials per clock are one of the bounds where the streams are row
+        // tiles: there one pair in eight goes to the FMA pipe (8192-token prompt 834 -> 804 us; one in
+        // four 820, three in eight 850; at 256 values it only costs issue slots).
+        if (!Cfg<D>::kSplitKV && n == 6) {
+          x = exp2_poly(x);
+        } else {
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+        }
         sum = add_f32x2(sum, x);
         p[16 * i + 8 * g + n / 2] = pack_f16(x.x, x.y);
       }
@@ -641,71 +674,64 @@ __device__ __forceinline__ bool stream_any(int w, bool any) {
   return r != 0;
 }
 
-// The CTA's query rows in two E4M3 parts, scaled by 2^-e; a warp takes whole rows.
+// The CTA's query rows in two E4M3 parts, scaled by 2^-e.  A lane holds 16 consecutive values,
+// one piece of each part, so D / 16 lanes take a row and a warp several rows at a time.
 template <int D>
-__device__ void load_queries(const Args &a, Control<D> &c, unsigned char *qbuf, const Item &it, int warp) {
+__device__ __forceinline__ void load_queries(const Args &a, Control<D> &c, unsigned char *qbuf, const Item &it, int warp) {
   using C = Cfg<D>;
-  constexpr int N = D / 32;  // values per lane
-  constexpr int kDepth = 4;  // rows in flight
-  const int lane = threadIdx.x & 31, n_rows = it.sq.q_len * a.group;
-  constexpr int kPer = C::ROWS / (kSoftmax / 32);
+  constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes;
+  constexpr int kPer = C::ROWS / (kSoftmax / 32), kSteps = kPer / kRowsAtOnce;  // rows of a warp, in steps
+  const int lane = threadIdx.x & 31, piece = lane % kLanes;
+  const int n_rows = it.sq.q_len * a.group;
   const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
-#pragma unroll 1
-  for (int r0 = warp * kPer; r0 < (warp + 1) * kPer; r0 += kDepth) {
-    uint32_t raw[kDepth][N / 2];
+  uint4 raw[kSteps][2];
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int R = it.row0 + r0 + u;
-      const bool ok = R < n_rows;
-      const uint16_t *src = a.q + (it.sq.start + (ok ? R / a.group : 0)) * a.ld_q + int64_t(it.h * a.group + (ok ? R % a.group : 0)) * D + lane * N;
-      if constexpr (N == 8) {
-        const uint4 x = ok ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-        raw[u][0] = x.x, raw[u][1] = x.y, raw[u][2] = x.z, raw[u][3] = x.w;
-      } else if constexpr (N == 4) {
-        const uint2 x = ok ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
-        raw[u][0] = x.x, raw[u][1] = x.y;
-      } else {
-        raw[u][0] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      float amax = 0.0f;
-#pragma unroll
-      for (int n = 0; n < N / 2; ++n)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[u][n] << 16)), fabsf(__uint_as_float(raw[u][n] & 0xFFFF0000u))));
-      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // magnitudes order as integers
-      // 2^-e brings the largest magnitude into (224, 448], 448 = 1.75 * 2^8
-      const uint32_t bits = __float_as_uint(amax);
-      const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
-      // an infinite value makes every score of the row infinite or NaN: the row is NaN
-      const float f = bits < 0x7f800000u ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * sign : __int_as_float(0x7fffffff);
-      const int r = r0 + u, row = r & (kTile - 1);
-      if (lane == 0) c.rc[r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(min(e, 120) + 127) << 23);
-      uint16_t hi[N / 2], lo[N / 2];
-#pragma unroll
-      for (int n = 0; n < N / 2; ++n) {
-        const float x0 = __uint_as_float(raw[u][n] << 16) * f, x1 = __uint_as_float(raw[u][n] & 0xFFFF0000u) * f;
-        hi[n] = cvt_e4m3x2(x1, x0);
-        const uint32_t back = e4m3x2_to_f16x2(hi[n]);
-        const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-        lo[n] = cvt_e4m3x2(x1 - hf.y, x0 - hf.x);
-      }
-      unsigned char *dst = qbuf + (r / kTile) * 2 * C::Q_PART + code_offset<D>(kTile, row, lane * N / 16) + (lane * N) % 16;
-      if constexpr (N == 8) {
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0] | uint32_t(hi[1]) << 16, hi[2] | uint32_t(hi[3]) << 16);
-        *reinterpret_cast<uint2 *>(dst + C::Q_PART) = make_uint2(lo[0] | uint32_t(lo[1]) << 16, lo[2] | uint32_t(lo[3]) << 16);
-      } else if constexpr (N == 4) {
-        *reinterpret_cast<uint32_t *>(dst) = hi[0] | uint32_t(hi[1]) << 16;
-        *reinterpret_cast<uint32_t *>(dst + C::Q_PART) = lo[0] | uint32_t(lo[1]) << 16;
-      } else {
-        *reinterpret_cast<uint16_t *>(dst) = hi[0];
-        *reinterpret_cast<uint16_t *>(dst + C::Q_PART) = lo[0];
-      }
+  for (int u = 0; u < kSteps; ++u) {
+    const int R = it.row0 + warp * kPer + u * kRowsAtOnce + lane / kLanes;
+    raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+    if (R < n_rows) {
+      const int t = R / a.group;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          a.q + (it.sq.start + t) * a.ld_q + int64_t(it.h * a.group + (R - t * a.group)) * D + 16 * piece);
+      raw[u][0] = __ldg(src);
+      raw[u][1] = __ldg(src + 1);
     }
   }
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const uint32_t v[8] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w, raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
+    uint32_t top = 0;  // BF16 magnitudes order as integers, two at a time
+#pragma unroll
+    for (int n = 0; n < 8; ++n) top = __vmaxu2(top, v[n] & 0x7fff7fffu);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t bits = max(top & 0xffffu, top >> 16) << 16;  // the row's largest magnitude
+    // 2^-e brings it into (224, 448], 448 = 1.75 * 2^8
+    const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+    // an infinite value makes every score of the row infinite or NaN: the row is NaN
+    const float f = bits < 0x7f800000u ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * sign : __int_as_float(0x7fffffff);
+    const int r = warp * kPer + u * kRowsAtOnce + lane / kLanes;
+    if (piece == 0) c.rc[r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(min(e, 120) + 127) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      hi[n] = lo[n] = 0;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t x = v[2 * n + m];
+        const float x0 = __uint_as_float(x << 16) * f, x1 = __uint_as_float(x & 0xFFFF0000u) * f;
+        const uint32_t c8 = cvt_e4m3x2(x1, x0), back = e4m3x2_to_f16x2(c8);
+        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+        hi[n] |= c8 << (16 * m);
+        lo[n] |= static_cast<uint32_t>(cvt_e4m3x2(x1 - h.y, x0 - h.x)) << (16 * m);
+      }
+    }
+    unsigned char *dst = qbuf + (r / kTile) * 2 * C::Q_PART + code_offset<D>(kTile, r & (kTile - 1), piece);
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(dst + C::Q_PART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
   fence_async_smem();
-  mbar_arrive(&c.q_ready);
+  warp_arrive(&c.q_ready);
 }
 
 // Softmax warpgroup of half `hf` of stream w; tid 0..127 is the row of its tile.
@@ -789,27 +815,26 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
     l += add;
     if constexpr (C::kSplitKV) {
       if (hf == 0) c.m_ref[j & 1][tid] = m_ref;  // read last for tile j - 1, whose both halves arrived
-      mbar_arrive(&c.m_ready[w]);
+      warp_arrive(&c.m_ready[w]);
     }
     if (ok) {
       store_p(s_tmem, p);
       tmem_st_wait();
       tc_fence_before();
-      __syncwarp();
-      if ((tid & 31) == 0) mbar_arrive(&c.p_ready[sl]);
+      warp_arrive(&c.p_ready[sl]);
     }
   }
 
   // Join the partial sums, then O / l.
   if constexpr (C::kSplitKV) {
-    mbar_arrive(&c.join);
+    warp_arrive(&c.join);
     ok = ok && mbar_wait(&c.join, 0);
     const float m = c.m_ref[(n_tiles - 1) & 1][tid];  // the last reference; l is relative to the one seen last
     if (m != m_ref && m_ref != -INFINITY) l *= ex2(m_ref - m);
     m_ref = m;
   }
   c.l[2 * w + hf][tid] = l;
-  mbar_arrive(&c.join);
+  warp_arrive(&c.join);
   ok = ok && mbar_wait(&c.join, C::kSplitKV ? 1 : 0);
   l = c.l[2 * w][tid] + c.l[2 * w + 1][tid];
   if constexpr (C::kSplitKV) l += c.l[2 * (w ^ 1)][tid] + c.l[2 * (w ^ 1) + 1][tid];
@@ -879,13 +904,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   unsigned char *qbuf = smem, *kbuf = smem + C::K_OFF, *vbuf = smem + C::V_OFF, *raw = smem + C::RAW_OFF;
   Control<D> &c = *reinterpret_cast<Control<D> *>(smem + C::CTL_OFF);
   if (tid == 0) {
-    mbar_init(&c.q_ready, kSoftmax);
+    mbar_init(&c.q_ready, kSoftmax / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.raw_full[i], 1);
-      mbar_init(&c.raw_empty[i], 128);
+      mbar_init(&c.raw_empty[i], 4);
       mbar_init(&c.v_full[i], 128);
       mbar_init(&c.v_empty[i], 1);
-      mbar_init(&c.m_ready[i], 256);
+      mbar_init(&c.m_ready[i], 8);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&c.k_full[i], 1);
@@ -896,8 +921,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&c.p_ready[i], 8);
       mbar_init(&c.o_done[i], 1);
     }
-    mbar_init(&c.join, kSoftmax);
-    mbar_init(&c.done, 2);
+    mbar_init(&c.join, kSoftmax / 32);
+    mbar_init(&c.done[0], 1);
+    mbar_init(&c.done[1], 1);
     fence_barrier_init();
     c.nan_any = 0;
   }
@@ -924,8 +950,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     } else if (warp != 3) {
       Issuer<D> mma(c, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf));
       mma.run(warp >> 1, __reduce_max_sync(0xffffffffu, n_tiles));  // uniform for the compiler too
-      commit(mma.elected, &c.done);  // whatever was issued has to end before TMEM is given back
-      mbar_wait(&c.done, 0);
+      if (C::kSplitKV || warp == 0) {  // whatever was issued has to end before TMEM is given back
+        commit(mma.elected, &c.done[warp >> 1]);
+        mbar_wait(&c.done[warp >> 1], 0);
+      }
     }
   }
   __syncwarp();
