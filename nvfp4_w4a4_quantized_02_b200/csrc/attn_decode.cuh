@@ -8,10 +8,12 @@
 //     P_j = 2^{x_j + log2 sV_j - M + kBoost},
 // already hold the value scale and are at most 2^kBoost, while the denominator adds
 // P_j / sV_j.  kBoost keeps weights down to 2^-36 of the largest above the FP16 subnormals.
+// M need not be the maximum itself: it follows when a weight would exceed 2^(kBoost + kSlack).
 //
-// Bound by HBM: every cached byte is read once per kv head, for 2 x 8 multiply-adds.  So
-// K and V go from global memory straight into registers in the layout that
-// mma.m16n8k16 wants, with no trip through shared memory:
+// Bound by HBM: every cached byte is read once per kv head, for 2 x 8 multiply-adds.  Each warp
+// keeps its own ring of STAGES steps of K and V rows in shared memory, filled by TMA, so that
+// about 190 KB are on their way to an SM whatever its warps do (loads straight into registers reached
+// 3.3 TB/s on 32 sequences of up to 8192 tokens), and feeds mma.m16n8k16 from it:
 //  * S^T = K Q^T has the cached tokens as its 16 rows and up to 8 query rows (the heads of
 //    a group, times tokens) as its 8 columns.  The contraction runs over the head's
 //    values in any order as long as K and Q agree, so a lane takes 16 consecutive bytes
@@ -20,6 +22,8 @@
 //    reads the same 16 values of four tokens and byte permutes pair the tokens.  The
 //    accumulators' columns are query rows again, so rescaling is lane-local, and
 //    movmatrix turns S^T's accumulators into the P^T operand.
+// The 16 tokens of a tile may stand in any order in both products; with the 128-byte swizzle of
+// the TMA and the order of token_of() every shared-memory read is free of bank conflicts.
 // E4M3 is exact in FP16; q is scaled by a power of two per row to lie in FP16's range
 // and keeps all of its BF16 bits within 2^-29 of the row's largest value.  Sums, maxima
 // and accumulators are FP32.
@@ -31,6 +35,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -40,6 +46,7 @@ constexpr int kRows = 8;        // query rows of a unit
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kBoost = 12.0f;
+constexpr float kSlack = 3.0f;
 constexpr float kMinLogScale = -100.0f;  // log2 of the smallest value scale taken at its word
 constexpr int kGroup = 16;      // tokens of one mma tile; a cache block holds a multiple of it
 
@@ -72,22 +79,62 @@ struct Args {
   int max_decode_rows;        // sequences with more query rows per kv head belong to the prompt kernel
 };
 
+// log2 of the tokens of a warp's step.
+__host__ __device__ constexpr int step_log(int d) { return d == 256 ? 4 : 5; }
+
 template <int D>
 struct Cfg {
-  static constexpr int TS = D == 256 ? 16 : 32;  // tokens of a warp's step
+  static constexpr int TS = 1 << step_log(D);
   static constexpr int NG = TS / kGroup;
+  static constexpr int STAGES = D == 256 ? 3 : 2;  // steps of a warp's ring
+  static constexpr int CTAS = D == 256 ? 2 : 3;    // per SM
   static constexpr int TILE = TS * kWarps;       // tokens of a CTA's step
   static constexpr int SEGK = D / 64;            // 64-value segments of a K row
   static constexpr int VW = D >= 128 ? 4 : 2;    // 32-bit words of V per lane and token, per segment
   static constexpr int SEGV = D >= 128 ? D / 128 : 1;
   static constexpr int MB = D / 16;              // 16-value row blocks of O^T
   static constexpr int LD = D + 4;
+  static constexpr int ROWB = D < 128 ? D : 128;  // bytes of a row of a panel
+  static constexpr int PANELS = D / ROWB;
+  static constexpr int PART = TS * D;            // bytes of a step's K (or V)
+  static constexpr int RING = kWarps * STAGES * 2 * PART;
 };
+
+// Rows of a TMA box of codes: a power of two of tokens of one cache block, up to a step.
+__host__ __device__ constexpr int box_log(int log_block, int d) { return log_block < step_log(d) ? log_block : step_log(d); }
+
+// Token of row `slot` of a 16-token tile: 0 5 2 7 4 1 6 3, then the same plus 8.
+__device__ __forceinline__ int token_of(int slot) { return slot & 1 ? (((slot & 6) ^ 4) + 1) | (slot & 8) : slot; }
+
+// Byte offset of 16-byte piece c of row r in a panel, as the TMA's swizzle puts it.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return D < 128 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_bytes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two_bytes)));
   return r;
+}
+
+// Four codes of a word as two FP16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -115,21 +162,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint4 ld_stream(const void *p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
+// log2 of a value scale, exact for powers of two; scales below 2^kMinLogScale count as that.
+__device__ __forceinline__ float log_scale(float s) {
+  const uint32_t b = __float_as_uint(s);
+  if (b < (uint32_t(127 + int(kMinLogScale)) << 23)) return kMinLogScale;
+  float f;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(f) : "f"(__uint_as_float((b & 0x7fffffu) | 0x3f800000u)));
+  if ((b & 0x7fffffu) == 0) f = 0.0f;
+  return b < 0x7f800000u ? float(int(b >> 23) - 127) + f : __int_as_float(0x7fffffff);
 }
-__device__ __forceinline__ uint2 ld_stream2(const void *p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
-
-// log2 of a value scale, exact for powers of two.
-__device__ __forceinline__ float log_scale(float s) { return fmaxf(log2f(s), kMinLogScale) + (s != s ? s : 0.0f); }
+__device__ __forceinline__ float inverse_scale(float s) { return 1.0f / fmaxf(s, 0x1p-100f); }
 
 // Power of two 2^e that brings a row's largest magnitude into [2^14, 2^15) when the row is
 // multiplied by 2^-e; 0 for zero and non-finite rows.
@@ -157,9 +199,11 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int s) {
   return r;
 }
 
+// Shared memory behind the rings; the warps' O are joined in the rings' place.
 template <int D>
 struct DecodeSmem {
-  float o[kWarps][kRows][Cfg<D>::LD];
+  uint64_t full[kWarps][Cfg<D>::STAGES];
+  float4 scales[kWarps][Cfg<D>::STAGES][Cfg<D>::NG];  // (sK, log2 sV, 1 / sV, -) of each 16-token tile; sK < 0: no tokens there
   float m[kWarps][kRows], l[kWarps][kRows];
   int lim[kRows];
   int nan_first[D];  // first token, among those that some rows of the unit do not see, whose value is NaN
@@ -202,71 +246,70 @@ __device__ __forceinline__ void block_scan(int64_t &t, int64_t &u, int64_t *st, 
   }
 }
 
+// A warp's ring.  Lane i < boxes looks up and copies box i of a step (R tokens of one block, K
+// and V); it does so for step n + STAGES when step n is done, with the block number fetched one
+// step earlier.  The box's scales are written at the end of step n + 1, when they have arrived.
 template <int D>
-struct KStage {
-  uint4 r[Cfg<D>::NG][2][Cfg<D>::SEGK];
-};
-template <int D>
-struct VStage {
-  uint32_t r[Cfg<D>::NG][4][Cfg<D>::SEGV][Cfg<D>::VW];
-};
-
-// Where a 16-token group lives: its block's (block, head) index, or -1.
-template <int D>
-__device__ __forceinline__ int64_t group_block(const Args &a, int s, int h, int tok, int kv_len) {
-  if (tok >= kv_len) return -1;
-  const int64_t id = __ldg(a.table + s * a.ld_table + (tok >> a.log_block));
-  if (id < 0 || id >= a.num_blocks) {
-    record_bad_index();
-    return -1;
-  }
-  return id * a.kv_heads + h;
-}
-
-template <int D>
-__device__ __forceinline__ void load_k(const Args &a, uint4 (&r)[2][Cfg<D>::SEGK], int64_t blk, int tok, int kv_len) {
-  const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
-  const int off = tok & ((1 << a.log_block) - 1);
-  const uint8_t *p = a.k + ((blk << a.log_block) + off + g) * D + 16 * q;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int s = 0; s < Cfg<D>::SEGK; ++s)
-      r[i][s] = blk >= 0 && tok + g + 8 * i < kv_len ? ld_stream(p + i * 8 * D + s * 64) : make_uint4(0, 0, 0, 0);
-}
-
-template <int D>
-__device__ __forceinline__ void load_v(const Args &a, uint32_t (&r)[4][Cfg<D>::SEGV][Cfg<D>::VW], int64_t blk, int tok,
-                                       int kv_len) {
+struct Ring {
   using C = Cfg<D>;
-  const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
-  const int off = tok & ((1 << a.log_block) - 1);
-  const uint8_t *p = a.v + ((blk << a.log_block) + off) * D + 4 * C::VW * g;
+  const Args &a;
+  const CUtensorMap *k_map, *v_map;
+  unsigned char *buf;  // STAGES steps of K, V
+  uint64_t *full;
+  float4 (*scales)[C::NG];
+  int s, h, log_r, lane;
+  int end;        // tokens from here on are not wanted
+  bool mine;      // this lane has a box
+
+  // Number of the block that holds this lane's box of the step at token `tok`; -1: not wanted.
+  __device__ __forceinline__ int lookup(int tok) const {
+    const int t = tok + (lane << log_r);
+    return mine && t < end ? __ldg(a.table + s * a.ld_table + (t >> a.log_block)) : -1;
+  }
+  // Copies the step at token `tok`; returns the box's scales (sK < 0: no tokens there).
+  __device__ __forceinline__ float2 copy(int stage, int tok, int id) const {
+    float2 sc = make_float2(-1.0f, 1.0f);
+    if (tok >= end) return sc;  // uniform over the warp
+    const int t = tok + (lane << log_r);
+    int blk = -1;
+    if (mine && t < end) {
+      if (id >= 0 && id < a.num_blocks) blk = id * a.kv_heads + h;
+      else record_bad_index();
+    }
+    const uint32_t have = __ballot_sync(0xffffffffu, blk >= 0);
+    if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(have) * ((2 * D) << log_r));
+    __syncwarp();
+    if (blk >= 0) {
+      unsigned char *dst = buf + stage * 2 * C::PART + (lane << log_r) * C::ROWB;
+      const int row = t & ((1 << a.log_block) - 1);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int tt = 2 * q + (t & 1) + 8 * (t >> 1);  // tokens 2q, 2q + 1, 2q + 8, 2q + 9
-    const bool ok = blk >= 0 && tok + tt < kv_len;  // bytes behind the sequence never reach the product
-#pragma unroll
-    for (int s = 0; s < C::SEGV; ++s) {
-      if constexpr (C::VW == 4) {
-        const uint4 x = ok ? ld_stream(p + int64_t(tt) * D + s * 128) : make_uint4(0, 0, 0, 0);
-        r[t][s][0] = x.x, r[t][s][1] = x.y, r[t][s][2] = x.z, r[t][s][3] = x.w;
-      } else {
-        const uint2 x = ok ? ld_stream2(p + int64_t(tt) * D) : make_uint2(0, 0);
-        r[t][s][0] = x.x, r[t][s][1] = x.y;
+      for (int p = 0; p < C::PANELS; ++p) {
+        tma_load_3d(dst + p * C::TS * C::ROWB, k_map, full + stage, p * C::ROWB, row, blk);
+        tma_load_3d(dst + C::PART + p * C::TS * C::ROWB, v_map, full + stage, p * C::ROWB, row, blk);
       }
+      sc = make_float2(__ldg(a.k_scales + blk), __ldg(a.v_scales + blk));
+    }
+    return sc;
+  }
+  __device__ __forceinline__ void write_scales(int stage, float2 sc) const {
+    if (mine) {
+      const float4 v = make_float4(sc.x, log_scale(sc.y), inverse_scale(sc.y), 0.0f);
+      for (int g = 0; g < (1 << log_r) / kGroup; ++g) scales[stage][(lane << log_r) / kGroup + g] = v;
     }
   }
-}
+};
 
 // One segment of a unit: cached tiles [tile0, tile0 + ntile) of (sequence s, kv head h,
 // row group rg).  `slot` < 0: the segment is the whole unit and its result goes to `out`,
 // else to partial `slot` of the workspace.
 template <int D>
-__device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, int s, int h, int rg, int tile0,
+__device__ bool decode_segment(const Args &a, const CUtensorMap *k_map, const CUtensorMap *v_map, DecodeSmem<D> &sm,
+                               unsigned char *rings, uint32_t &phases, const Seq &sq, int s, int h, int rg, int tile0,
                                int ntile, int slot) {
   using C = Cfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char *buf = rings + warp * (Cfg<D>::STAGES * 2 * C::PART);
+  bool ok = true;
   const int g = lane >> 2, q = lane & 3;
   const int n_rows = min(kRows, sq.q_len * a.group - rg * kRows);
 
@@ -276,6 +319,19 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
     sm.lim[threadIdx.x] = a.causal ? min(sq.kv_len, sq.kv_len - sq.q_len + R / a.group + 1) : sq.kv_len;
   }
   for (int i = threadIdx.x; i < D; i += kThreads) sm.nan_first[i] = 0x7fffffff;
+
+  const int last_row = rg * kRows + n_rows - 1;  // the unit's rows are in token order: it sees most
+  const int kv_end = a.causal ? min(sq.kv_len, sq.kv_len - sq.q_len + last_row / a.group + 1) : sq.kv_len;
+  const int tok_end = min((tile0 + ntile) * C::TILE, kv_end);
+  const int log_r = box_log(a.log_block, D), tok0 = (tile0 * kWarps + warp) * C::TS;
+  const Ring<D> ring{a, k_map, v_map, buf, sm.full[warp], sm.scales[warp], s, h, log_r, lane, tok_end, (lane << log_r) < C::TS};
+  int id[C::STAGES + 1];
+  float2 pending[C::STAGES];
+#pragma unroll
+  for (int i = 0; i <= C::STAGES; ++i) id[i] = ring.lookup(tok0 + i * C::TILE);
+#pragma unroll
+  for (int i = 0; i < C::STAGES; ++i) pending[i] = ring.copy(i, tok0 + i * C::TILE, id[i]);
+  int next_id = id[C::STAGES];
 
   // Q fragments of row g: values 64 seg + 16 q + 4 j + {0, 1 | 2, 3}, scaled by 2^-e.
   uint32_t qf[C::SEGK][4][2];
@@ -317,8 +373,7 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
   const float rc0 = __shfl_sync(0xffffffffu, rc, 8 * q), rc1 = __shfl_sync(0xffffffffu, rc, 8 * q + 4);
   __syncthreads();
   const int lim0 = sm.lim[2 * q], lim1 = sm.lim[2 * q + 1];
-  const int lim_min = sm.lim[0], lim_max = sm.lim[kRows - 1];  // rows are in token order
-  const int kv_end = min(sq.kv_len, lim_max);
+  const int lim_min = min(sm.lim[0], tok_end);
 
   float o[C::MB][4];
 #pragma unroll
@@ -327,127 +382,153 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
     for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 
-  int tok = (tile0 * kWarps + warp) * C::TS;
-  const int tok_end = min((tile0 + ntile) * C::TILE, kv_end);
-  KStage<D> ks;
-  int64_t blk[C::NG];
 #pragma unroll
-  for (int n = 0; n < C::NG; ++n) {
-    blk[n] = group_block<D>(a, s, h, tok + kGroup * n, min(kv_end, tok_end));
-    load_k<D>(a, ks.r[n], blk[n], tok + kGroup * n, kv_end);
-  }
-  for (; tok < tok_end; tok += C::TILE) {
-    VStage<D> vs;
-    float sk[C::NG], sv[C::NG];
+  for (int i = 0; i < C::STAGES; ++i) ring.write_scales(i, pending[i]);
+  __syncwarp();
+  int stage = 0, last = -1;  // last: stage of the scales on their way
+  float2 sc_last = make_float2(0.0f, 0.0f);
+  const int tk = token_of(g);
+#pragma unroll 1
+  for (int tok = tok0; tok < tok_end; tok += C::TILE) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[warp][stage], (phases >> stage) & 1));
+    if (!ok) break;
+    phases ^= 1u << stage;
+    const unsigned char *kb = buf + stage * 2 * C::PART, *vb = kb + C::PART;
+    float4 sc[C::NG];
 #pragma unroll
-    for (int n = 0; n < C::NG; ++n) {
-      load_v<D>(a, vs.r[n], blk[n], tok + kGroup * n, kv_end);
-      sk[n] = blk[n] >= 0 ? __ldg(a.k_scales + blk[n]) : 0.0f;
-      sv[n] = blk[n] >= 0 ? __ldg(a.v_scales + blk[n]) : 1.0f;
-    }
-    int64_t nblk[C::NG];
-#pragma unroll
-    for (int n = 0; n < C::NG; ++n) nblk[n] = group_block<D>(a, s, h, tok + C::TILE + kGroup * n, tok_end);
+    for (int n = 0; n < C::NG; ++n) sc[n] = sm.scales[warp][stage][n];
 
-    float x[C::NG][4];
+    // A step whose tokens all rows see needs no masks.
+    bool tail = tok + C::TS > lim_min;
 #pragma unroll
-    for (int n = 0; n < C::NG; ++n) {
+    for (int n = 0; n < C::NG; ++n) tail |= sc[n].x < 0.0f;
+    auto step = [&](auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      float x[C::NG][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[n][j] = 0.0f;
+      for (int n = 0; n < C::NG; ++n) {
 #pragma unroll
-      for (int i = 0; i < C::SEGK; ++i) {
-        const uint32_t ka[4] = {ks.r[n][0][i].x, ks.r[n][0][i].y, ks.r[n][0][i].z, ks.r[n][0][i].w};
-        const uint32_t kb[4] = {ks.r[n][1][i].x, ks.r[n][1][i].y, ks.r[n][1][i].z, ks.r[n][1][i].w};
+        for (int j = 0; j < 4; ++j) x[n][j] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_f16(x[n], e4m3x2_to_f16x2(ka[j]), e4m3x2_to_f16x2(kb[j]), e4m3x2_to_f16x2(ka[j] >> 16),
-                  e4m3x2_to_f16x2(kb[j] >> 16), qf[i][j][0], qf[i][j][1]);
+        for (int i = 0; i < C::SEGK; ++i) {
+          const int panel = i * 64 / C::ROWB, piece = (i * 64 % C::ROWB) / 16 + q;
+          const unsigned char *base = kb + panel * C::TS * C::ROWB;
+          const uint4 lo = *reinterpret_cast<const uint4 *>(base + swizzled<D>(kGroup * n + tk, piece));
+          const uint4 hi = *reinterpret_cast<const uint4 *>(base + swizzled<D>(kGroup * n + tk + 8, piece));
+          const uint32_t ka[4] = {lo.x, lo.y, lo.z, lo.w}, kc[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(ka[j], a0, a2);
+            e4m3x4_to_f16x4(kc[j], a1, a3);
+            mma_f16(x[n], a0, a1, a2, a3, qf[i][j][0], qf[i][j][1]);
+          }
+        }
       }
-    }
-#pragma unroll
-    for (int n = 0; n < C::NG; ++n) load_k<D>(a, ks.r[n], nblk[n], tok + C::TILE + kGroup * n, kv_end);
 
-    float mx0 = m0, mx1 = m1, inv[C::NG];
+      float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < C::NG; ++n) {
-      const float e = log_scale(sv[n]);
-      inv[n] = exp2f(-e);
-      const float c0 = sk[n] * rc0, c1 = sk[n] * rc1;
-      const int t0 = blk[n] >= 0 ? tok + kGroup * n + g : 0x7fffffff - 8;
-      x[n][0] = t0 < lim0 ? fmaf(x[n][0], c0, e) : -INFINITY;
-      x[n][1] = t0 < lim1 ? fmaf(x[n][1], c1, e) : -INFINITY;
-      x[n][2] = t0 + 8 < lim0 ? fmaf(x[n][2], c0, e) : -INFINITY;
-      x[n][3] = t0 + 8 < lim1 ? fmaf(x[n][3], c1, e) : -INFINITY;
-      mx0 = fmaxf(mx0, fmaxf(x[n][0], x[n][2]));
-      mx1 = fmaxf(mx1, fmaxf(x[n][1], x[n][3]));
-    }
-#pragma unroll
-    for (int w = 4; w < 32; w <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, w));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, w));
-    }
-    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-      const float f0 = mx0 > m0 ? ex2(m0 - mx0) : 1.0f, f1 = mx1 > m1 ? ex2(m1 - mx1) : 1.0f;
-      m0 = mx0, m1 = mx1;
-      l0 *= f0, l1 *= f1;
-#pragma unroll
-      for (int i = 0; i < C::MB; ++i) {
-        o[i][0] *= f0, o[i][1] *= f1;
-        o[i][2] *= f0, o[i][3] *= f1;
+      for (int n = 0; n < C::NG; ++n) {
+        const float c0 = sc[n].x * rc0, c1 = sc[n].x * rc1, e = sc[n].y;
+        x[n][0] = fmaf(x[n][0], c0, e);
+        x[n][1] = fmaf(x[n][1], c1, e);
+        x[n][2] = fmaf(x[n][2], c0, e);
+        x[n][3] = fmaf(x[n][3], c1, e);
+        if constexpr (MASK) {
+          const bool none = sc[n].x < 0.0f || tok + kGroup * n >= tok_end;
+          const int t0 = none ? 0x7fffffff - 8 : tok + kGroup * n + tk;
+          x[n][0] = t0 < lim0 ? x[n][0] : -INFINITY;
+          x[n][1] = t0 < lim1 ? x[n][1] : -INFINITY;
+          x[n][2] = t0 + 8 < lim0 ? x[n][2] : -INFINITY;
+          x[n][3] = t0 + 8 < lim1 ? x[n][3] : -INFINITY;
+        }
+        mx0 = fmaxf(mx0, fmaxf(x[n][0], x[n][2]));
+        mx1 = fmaxf(mx1, fmaxf(x[n][1], x[n][3]));
       }
-    }
-    const float b0 = (m0 == -INFINITY ? 0.0f : m0) - kBoost, b1 = (m1 == -INFINITY ? 0.0f : m1) - kBoost;
-    uint32_t pf[C::NG][2];
+      // The reference stays while no weight exceeds 2^(kBoost + kSlack).
+      if (__any_sync(0xffffffffu, mx0 > m0 + kSlack || mx1 > m1 + kSlack)) {
 #pragma unroll
-    for (int n = 0; n < C::NG; ++n) {
-      const float p0 = ex2(x[n][0] - b0), p1 = ex2(x[n][1] - b1), p2 = ex2(x[n][2] - b0), p3 = ex2(x[n][3] - b1);
-      l0 = fmaf(p0 + p2, inv[n], l0);
-      l1 = fmaf(p1 + p3, inv[n], l1);
-      pf[n][0] = movmatrix_trans(pack_f16(p0, p1));
-      pf[n][1] = movmatrix_trans(pack_f16(p2, p3));
-    }
-    // Tokens that only some of the rows see: a NaN value there must not reach the rows that
-    // do not (their weight is 0, and 0 * NaN is NaN), so it is taken out of the product
-    // and its place remembered.
-    if (tok + C::TS > lim_min) {
+        for (int w = 4; w < 32; w <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, w));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, w));
+        }
+        const float f0 = mx0 > m0 ? ex2(m0 - mx0) : 1.0f, f1 = mx1 > m1 ? ex2(m1 - mx1) : 1.0f;
+        m0 = fmaxf(m0, mx0), m1 = fmaxf(m1, mx1);
+        l0 *= f0, l1 *= f1;
+#pragma unroll
+        for (int i = 0; i < C::MB; ++i) {
+          o[i][0] *= f0, o[i][1] *= f1;
+          o[i][2] *= f0, o[i][3] *= f1;
+        }
+      }
+      const float b0 = (m0 == -INFINITY ? 0.0f : m0) - kBoost, b1 = (m1 == -INFINITY ? 0.0f : m1) - kBoost;
+      uint32_t pf[C::NG][2];
+#pragma unroll
+      for (int n = 0; n < C::NG; ++n) {
+        const float p0 = ex2(x[n][0] - b0), p1 = ex2(x[n][1] - b1), p2 = ex2(x[n][2] - b0), p3 = ex2(x[n][3] - b1);
+        l0 = fmaf(p0 + p2, sc[n].z, l0);
+        l1 = fmaf(p1 + p3, sc[n].z, l1);
+        pf[n][0] = movmatrix_trans(pack_f16(p0, p1));
+        pf[n][1] = movmatrix_trans(pack_f16(p2, p3));
+      }
+      // V: a lane's 16 (at 64 values 8) values of its four tokens of each tile.
 #pragma unroll
       for (int n = 0; n < C::NG; ++n)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int i = 0; i < C::SEGV; ++i) {
+          uint32_t r[4][C::VW];
 #pragma unroll
-          for (int i = 0; i < C::SEGV; ++i)
-#pragma unroll
-            for (int w = 0; w < C::VW; ++w) {
-              uint32_t &word = vs.r[n][t][i][w];
-              if ((((word & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) == 0) continue;
-              const int tt = tok + kGroup * n + 2 * q + (t & 1) + 8 * (t >> 1);
-              for (int b = 0; b < 4; ++b)
-                if (((word >> (8 * b)) & 0x7f) == 0x7f) {
-                  atomicMin(&sm.nan_first[i * 128 + 4 * C::VW * g + 4 * w + b], tt);
-                  word &= ~(0xffu << (8 * b));
-                }
+          for (int t = 0; t < 4; ++t) {
+            const int row = kGroup * n + token_of(2 * q + (t & 1)) + 8 * (t >> 1);
+            if constexpr (C::VW == 4) {
+              const uint4 x4 = *reinterpret_cast<const uint4 *>(vb + i * C::TS * C::ROWB + swizzled<D>(row, g));
+              r[t][0] = x4.x, r[t][1] = x4.y, r[t][2] = x4.z, r[t][3] = x4.w;
+            } else {
+              const uint2 x2 = *reinterpret_cast<const uint2 *>(vb + swizzled<D>(row, g >> 1) + 8 * (g & 1));
+              r[t][0] = x2.x, r[t][1] = x2.y;
             }
-    }
+            // Bytes that belong to no token never reach the product.  Nor do, among tokens that only some
+            // of the rows see, NaN: the others' weight is 0, and 0 * NaN is NaN; its place is remembered.
+            if constexpr (MASK) {
+              const bool gone = sc[n].x < 0.0f || tok + row >= tok_end;
 #pragma unroll
-    for (int n = 0; n < C::NG; ++n)
+              for (int w = 0; w < C::VW; ++w) {
+                uint32_t &word = r[t][w];
+                if (gone) word = 0;
+                if ((((word & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) == 0) continue;
+                for (int b = 0; b < 4; ++b)
+                  if (((word >> (8 * b)) & 0x7f) == 0x7f) {
+                    atomicMin(&sm.nan_first[i * 128 + 4 * C::VW * g + 4 * w + b], tok + row);
+                    word &= ~(0xffu << (8 * b));
+                  }
+              }
+            }
+          }
 #pragma unroll
-      for (int i = 0; i < C::SEGV; ++i)
+          for (int w = 0; w < C::VW; ++w) {
+            // tokens (0, 1) and (2, 3) of values (0, 1), then (2, 3) of the word
 #pragma unroll
-        for (int w = 0; w < C::VW; ++w) {
-          const uint32_t(&r)[4][C::SEGV][C::VW] = vs.r[n];
-          const uint32_t lo01 = __byte_perm(r[0][i][w], r[1][i][w], 0x5140);
-          const uint32_t lo23 = __byte_perm(r[2][i][w], r[3][i][w], 0x5140);
-          const uint32_t hi01 = __byte_perm(r[0][i][w], r[1][i][w], 0x7362);
-          const uint32_t hi23 = __byte_perm(r[2][i][w], r[3][i][w], 0x7362);
-          float(&oa)[4] = o[(i * C::VW + w) * 2], (&ob)[4] = o[(i * C::VW + w) * 2 + 1];
-          mma_f16(oa, e4m3x2_to_f16x2(lo01), e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo23),
-                  e4m3x2_to_f16x2(lo23 >> 16), pf[n][0], pf[n][1]);
-          mma_f16(ob, e4m3x2_to_f16x2(hi01), e4m3x2_to_f16x2(hi01 >> 16), e4m3x2_to_f16x2(hi23),
-                  e4m3x2_to_f16x2(hi23 >> 16), pf[n][0], pf[n][1]);
+            for (int v = 0; v < 2; ++v) {
+              const uint32_t sel = v == 0 ? 0x5140 : 0x7362;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x4(__byte_perm(r[0][w], r[1][w], sel), a0, a1);
+              e4m3x4_to_f16x4(__byte_perm(r[2][w], r[3][w], sel), a2, a3);
+              mma_f16(o[(i * C::VW + w) * 2 + v], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+            }
+          }
         }
-#pragma unroll
-    for (int n = 0; n < C::NG; ++n) blk[n] = nblk[n];
+    };
+    if (tail) step(std::true_type{});
+    else step(std::false_type{});
+    if (last >= 0) ring.write_scales(last, sc_last);
+    __syncwarp();  // the stage has been read, and the scales are there before their step
+    const int ahead = tok + C::STAGES * C::TILE;
+    last = ahead < tok_end ? stage : -1;
+    sc_last = ring.copy(stage, ahead, next_id);
+    next_id = ring.lookup(ahead + C::TILE);
+    stage = stage + 1 == Cfg<D>::STAGES ? 0 : stage + 1;
   }
+  if (__syncthreads_or(!ok)) return false;  // a copy never came; the rings are in use no more
 
   // Join the warps: (O, M, l) of each through shared memory.
 #pragma unroll
@@ -455,6 +536,7 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
     l0 += __shfl_xor_sync(0xffffffffu, l0, w);
     l1 += __shfl_xor_sync(0xffffffffu, l1, w);
   }
+  float (*so)[kRows][C::LD] = reinterpret_cast<float (*)[kRows][C::LD]>(rings);
   if (g == 0) {
     sm.m[warp][2 * q] = m0, sm.m[warp][2 * q + 1] = m1;
     sm.l[warp][2 * q] = l0, sm.l[warp][2 * q + 1] = l1;
@@ -467,7 +549,7 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j)  // accumulator (value 2 b + j / 2 of the word, row 2 q + j % 2)
-          sm.o[warp][2 * q + (j & 1)][i * 128 + 4 * C::VW * g + 4 * w + 2 * b + (j >> 1)] = o[(i * C::VW + w) * 2 + b][j];
+          so[warp][2 * q + (j & 1)][i * 128 + 4 * C::VW * g + 4 * w + 2 * b + (j >> 1)] = o[(i * C::VW + w) * 2 + b][j];
   __syncthreads();
   for (int idx = threadIdx.x; idx < kRows * (D / 2); idx += kThreads) {
     const int r = idx / (D / 2), c = (idx % (D / 2)) * 2;
@@ -481,8 +563,8 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
     for (int w = 0; w < kWarps; ++w) {
       const float f = ex2(sm.m[w][r] - base);
       l = fmaf(sm.l[w][r], f, l);
-      o0 = fmaf(sm.o[w][r][c], f, o0);
-      o1 = fmaf(sm.o[w][r][c + 1], f, o1);
+      o0 = fmaf(so[w][r][c], f, o0);
+      o1 = fmaf(so[w][r][c + 1], f, o1);
     }
     if (sm.nan_first[c] < sm.lim[r]) o0 = __int_as_float(0x7fffffff);
     if (sm.nan_first[c + 1] < sm.lim[r]) o1 = __int_as_float(0x7fffffff);
@@ -499,12 +581,21 @@ __device__ void decode_segment(const Args &a, DecodeSmem<D> &sm, const Seq &sq, 
         *reinterpret_cast<__nv_bfloat162 *>(static_cast<uint16_t *>(a.out) + at) = __floats2bfloat162_rn(o0 * f, o1 * f);
     }
   }
-  __syncthreads();  // sm is used again by the next segment
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings are written by copies again
+  __syncthreads();
+  return true;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ Args a) {
-  __shared__ DecodeSmem<D> sm;
+__global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
+    decode_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *rings = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(rings + Cfg<D>::RING);
+  if (threadIdx.x < kWarps * Cfg<D>::STAGES) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
+  fence_barrier_init();
+  __syncthreads();
+  uint32_t phases = 0;  // bit i: parity of the next phase of the warp's stage i
   grid_dep_wait();
   grid_dep_launch();
 
@@ -590,15 +681,29 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
       a.desc[before_u + unit] = make_int4(seq, h, rg, 0);
       a.desc2[before_u + unit] = make_int2(blockIdx.x, static_cast<int>(((last + 1) * ctas - 1) / total));
     }
-    decode_segment<D>(a, sm, sq, seq, h, rg, tile0, ntile, whole ? -1 : 2 * int(blockIdx.x) + (tile0 == 0));
+    if (!decode_segment<D>(a, &k_map, &v_map, sm, rings, phases, sq, seq, h, rg, tile0, ntile,
+                           whole ? -1 : 2 * int(blockIdx.x) + (tile0 == 0)))
+      return;
     at += ntile;
   }
 }
 
-// Joins the partial results of the units that several CTAs share.  Grid (units, kRows),
-// D / 2 threads: one query row, two values per thread.
 template <int D>
-__global__ void __launch_bounds__(D / 2) combine_kernel(const __grid_constant__ Args a) {
+constexpr int decode_smem_bytes() {
+  return 1024 + Cfg<D>::RING + int(sizeof(DecodeSmem<D>));
+}
+
+// Joins the partial results of the units that several CTAs share.  Grid (units, kRows / ROWS): D / 4
+// threads take four values each of a query row, for one in kJoin partials.
+template <int D>
+struct Join {
+  static constexpr int PARTS = 4, ROWS = 2, PER_ROW = D / 4, THREADS = ROWS * PER_ROW * PARTS;
+};
+template <int D>
+__global__ void __launch_bounds__(Join<D>::THREADS) combine_kernel(const __grid_constant__ Args a) {
+  constexpr int kJoin = Join<D>::PARTS, ROWS = Join<D>::ROWS;
+  __shared__ float4 so[kJoin][ROWS][D / 4];
+  __shared__ float sl[kJoin][ROWS], smax[kJoin][ROWS];
   grid_dep_wait();
   grid_dep_launch();
   if (int(blockIdx.x) >= *a.n_units) return;
@@ -606,30 +711,67 @@ __global__ void __launch_bounds__(D / 2) combine_kernel(const __grid_constant__ 
   if (c.x == c.y) return;  // one CTA wrote the result
   const int4 u = a.desc[blockIdx.x];
   const Seq sq = load_seq(a, u.x);
-  const int r = blockIdx.y, R = u.z * kRows + r;
-  if (R >= sq.q_len * a.group) return;
+  const int part = threadIdx.x / (ROWS * D / 4), r = threadIdx.x / (D / 4) % ROWS, col = threadIdx.x % (D / 4);
+  const int row = blockIdx.y * ROWS + r, R = u.z * kRows + row;
+  const bool valid = R < sq.q_len * a.group;  // other rows' partials are not written
   // the first CTA's partial is its last segment, the others' their first
-  auto slot = [&](int i) { return int64_t(2 * i + (i == c.x)) * kRows + r; };
-  float M = -INFINITY;
-  for (int i = c.x; i <= c.y; ++i) M = fmaxf(M, a.part_ml[slot(i)].x);
-  const float base = M == -INFINITY ? 0.0f : M;
-  float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll 4
-  for (int i = c.x; i <= c.y; ++i) {
-    const int64_t at = slot(i);
-    const float2 ml = a.part_ml[at];
-    const float2 o = *reinterpret_cast<const float2 *>(a.part + at * D + 2 * threadIdx.x);
-    const float f = ex2(ml.x - base);
-    l = fmaf(ml.y, f, l);
-    o0 = fmaf(o.x, f, o0);
-    o1 = fmaf(o.y, f, o1);
+  auto slot = [&](int i) { return int64_t(2 * i + (i == c.x)) * kRows + row; };
+  // every kJoin-th partial, with a running maximum; four loads in flight
+  float M = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = c.x + part; valid && i0 <= c.y; i0 += 4 * kJoin) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kJoin;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i <= c.y) {
+        ml[k] = a.part_ml[slot(i)];
+        v[k] = *reinterpret_cast<const float4 *>(a.part + slot(i) * D + 4 * col);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = fmaxf(m, ml[k].x);
+    const float base = m == -INFINITY ? 0.0f : m, g = ex2(M - base);
+    l *= g;
+    o.x *= g, o.y *= g, o.z *= g, o.w *= g;
+    M = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k * kJoin > c.y) continue;
+      const float f = ex2(ml[k].x - base);
+      l = fmaf(ml[k].y, f, l);
+      o.x = fmaf(v[k].x, f, o.x), o.y = fmaf(v[k].y, f, o.y), o.z = fmaf(v[k].z, f, o.z), o.w = fmaf(v[k].w, f, o.w);
+    }
+  }
+  so[part][r][col] = o;
+  if (col == 0) sl[part][r] = l, smax[part][r] = M;
+  __syncthreads();
+  if (part != 0 || !valid) return;
+  float m = smax[0][r];
+#pragma unroll
+  for (int k = 1; k < kJoin; ++k) m = fmaxf(m, smax[k][r]);
+  const float base = m == -INFINITY ? 0.0f : m;
+  l = 0.0f;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int k = 0; k < kJoin; ++k) {
+    const float f = ex2(smax[k][r] - base);
+    const float4 v = so[k][r][col];
+    l = fmaf(sl[k][r], f, l);
+    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
   }
   const float f = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (sq.start + R / a.group) * a.ld_out + int64_t(u.y * a.group + R % a.group) * D + 2 * threadIdx.x;
-  if (a.out_fp32)
-    *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(o0 * f, o1 * f);
-  else
-    *reinterpret_cast<__nv_bfloat162 *>(static_cast<uint16_t *>(a.out) + at) = __floats2bfloat162_rn(o0 * f, o1 * f);
+  const int64_t at = (sq.start + R / a.group) * a.ld_out + int64_t(u.y * a.group + R % a.group) * D + 4 * col;
+  if (a.out_fp32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  } else {
+    __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o.x * f, o.y * f), __floats2bfloat162_rn(o.z * f, o.w * f)};
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = *reinterpret_cast<const uint2 *>(p);
+  }
 }
 
 }  // namespace attn

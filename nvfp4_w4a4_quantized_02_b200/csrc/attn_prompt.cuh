@@ -63,6 +63,7 @@ struct Cfg {
   static constexpr int V_BYTES = BN * D * 2;
   static constexpr int K_STAGES = 3;
   static constexpr int GROUPS = BN / kGroup;
+  static constexpr int LOG_BOX = kSplitKV ? 6 : 7;     // rows of a TMA box at most: a tile
   static constexpr int CPR = D / 16;                   // 16-byte pieces of a row of codes
   static constexpr int PIECES = BN * CPR / 128;        // per converter thread
   static constexpr int ROWS = NQ * kTile;
@@ -179,15 +180,6 @@ __device__ __forceinline__ uint64_t sdesc_sw64_kmajor(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
-                                            int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -293,14 +285,14 @@ __device__ bool find_item(const Args &a, Item &it) {
   return false;
 }
 
-// Producer warp.  A tile consists of BN / R boxes of R consecutive tokens of one cache block
-// (R = min(block size, BN)); lane i looks up, and copies, box i.
+// Producer warp.  A tile consists of BN / R boxes of R consecutive tokens of one cache block; lane i
+// looks up, and copies, box i.
 template <int D>
 __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, unsigned char *kbuf, unsigned char *raw,
                         const Item &it, int n_tiles) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
-  const int log_r = min(a.log_block, C::kSplitKV ? 6 : 7), R = 1 << log_r, boxes = C::BN >> log_r;
+  const int log_r = min(a.log_block, C::LOG_BOX), R = 1 << log_r, boxes = C::BN >> log_r;
   const int mask = (1 << a.log_block) - 1;
   const int32_t *row = a.table + it.seq * a.ld_table;
   auto token = [&](int j) { return j * C::BN + (lane << log_r); };
@@ -326,7 +318,7 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
       Scales s;
       s.k = sk;
       s.log_v = blk >= 0 ? log_scale(sv) : -INFINITY;  // no such block: nothing to see
-      s.inv_v = blk >= 0 ? exp2f(-s.log_v) : 0.0f;
+      s.inv_v = blk >= 0 ? inverse_scale(sv) : 0.0f;
       s.pad = 0.0f;
       for (int g = 0; g < R / kGroup; ++g) c.ks[j & 7][lane * (R / kGroup) + g] = s;
     }
@@ -358,7 +350,7 @@ template <int D>
 __device__ void convert(const Args &a, Control<D> &c, const unsigned char *raw, unsigned char *vbuf, const Item &it,
                         int n_tiles, int tid) {
   using C = Cfg<D>;
-  const int log_r = min(a.log_block, C::kSplitKV ? 6 : 7);
+  const int log_r = min(a.log_block, C::LOG_BOX);
   const uint32_t all = C::BN >> log_r == 32 ? 0xffffffffu : (1u << (C::BN >> log_r)) - 1;
 #pragma unroll 1
   for (int j = 0; j < n_tiles; ++j) {

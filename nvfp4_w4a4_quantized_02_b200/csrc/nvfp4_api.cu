@@ -39,7 +39,6 @@ struct DeviceInfo {
   bool attrs = false;
   int quant_ctas_per_sm = 1;
   int gemm2_clusters = 1;  // co-resident 2-CTA clusters of gemm2_kernel
-  int attn_ctas_per_sm[3] = {1, 1, 1};  // of attn::decode_kernel at head size 64, 128, 256
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -83,6 +82,12 @@ nvfp4_status_t current_device(DeviceInfo **info) {
                              int(sizeof(gdn::Smem<32>))) != cudaSuccess ||
         cudaFuncSetAttribute(gdn::recurrence_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(sizeof(gdn::Smem<16>))) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::decode_smem_bytes<64>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::decode_smem_bytes<128>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::decode_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::decode_smem_bytes<256>()) != cudaSuccess ||
         cudaFuncSetAttribute(attn::prompt::prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              attn::prompt::smem_bytes<64>()) != cudaSuccess ||
         cudaFuncSetAttribute(attn::prompt::prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -112,13 +117,6 @@ nvfp4_status_t current_device(DeviceInfo **info) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, quantize_kernel, kQThreads, kQSmemBytes) != cudaSuccess)
       return NVFP4_ERR_CUDA;
     d.quant_ctas_per_sm = occ < 1 ? 1 : occ;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.attn_ctas_per_sm[0], attn::decode_kernel<64>, attn::kThreads,
-                                                      0) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.attn_ctas_per_sm[1], attn::decode_kernel<128>, attn::kThreads,
-                                                      0) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.attn_ctas_per_sm[2], attn::decode_kernel<256>, attn::kThreads,
-                                                      0) != cudaSuccess)
-      return NVFP4_ERR_CUDA;
     d.attrs = true;
   }
   *info = &d;
@@ -312,6 +310,22 @@ nvfp4_status_t check_batch(const nvfp4_batch_t *b, const nvfp4_block_cache_t *c,
       !aligned(c->v, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
     return NVFP4_ERR_MISALIGNED;
   return NVFP4_OK;
+}
+
+// Tensor map of the codes of K or V as [(block, head)][token][value], for boxes of 2^log_box of one
+// head's rows, up to 128 bytes wide and with the swizzle of that width (the layout of a K-major MMA
+// operand).  Encoded for every call: nothing is kept by a cache's address.
+bool encode_cache_map(CUtensorMap *m, uint8_t *codes, const nvfp4_block_cache_t *c, int log_box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int D = c->head_dim;
+  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(c->block_size), cuuint64_t(c->num_blocks * c->n_kv_heads)};
+  cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(c->block_size) * D};
+  cuuint32_t box[3] = {cuuint32_t(D < 128 ? D : 128), 1u << log_box, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Workspace of nvfp4_attention: unit count, unit descriptors, partial results.
@@ -1113,33 +1127,26 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   a.max_decode_rows = kDecodeRows;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int i = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
-  int ctas = dev->sms * dev->attn_ctas_per_sm[i];
+  int ctas = dev->sms * (i == 0 ? attn::Cfg<64>::CTAS : i == 1 ? attn::Cfg<128>::CTAS : attn::Cfg<256>::CTAS);
   if (ctas > kMaxAttnCtas) ctas = kMaxAttnCtas;
-  auto kernel = i == 0 ? attn::decode_kernel<64> : i == 1 ? attn::decode_kernel<128> : attn::decode_kernel<256>;
-  auto combine = i == 0 ? attn::combine_kernel<64> : i == 1 ? attn::combine_kernel<128> : attn::combine_kernel<256>;
-  if (nvfp4_status_t e = launch_pdl(kernel, dim3(ctas), dim3(attn::kThreads), 0, s, 1, a)) return e;
-  if (nvfp4_status_t e = launch_pdl(combine, dim3(static_cast<unsigned>(w.units), attn::kRows),
-                                    dim3(cache->head_dim / 2), 0, s, 1, a))
+  CUtensorMap k_map, v_map;
+  const int box = attn::box_log(log_block, cache->head_dim);
+  if (!encode_cache_map(&k_map, cache->k, cache, box) || !encode_cache_map(&v_map, cache->v, cache, box))
+    return NVFP4_ERR_CUDA;
+  auto launch_decode = [&](auto kernel, auto combine, int smem) {
+    if (nvfp4_status_t e = launch_pdl(kernel, dim3(ctas), dim3(attn::kThreads), smem, s, 1, a, k_map, v_map)) return e;
+    const int threads = i == 0 ? attn::Join<64>::THREADS : i == 1 ? attn::Join<128>::THREADS : attn::Join<256>::THREADS;
+    return launch_pdl(combine, dim3(static_cast<unsigned>(w.units), attn::kRows / attn::Join<128>::ROWS), dim3(threads), 0, s, 1, a);
+  };
+  if (nvfp4_status_t e = i == 0 ? launch_decode(attn::decode_kernel<64>, attn::combine_kernel<64>, attn::decode_smem_bytes<64>())
+                         : i == 1 ? launch_decode(attn::decode_kernel<128>, attn::combine_kernel<128>, attn::decode_smem_bytes<128>())
+                                  : launch_decode(attn::decode_kernel<256>, attn::combine_kernel<256>, attn::decode_smem_bytes<256>()))
     return e;
   // Only the device knows the sequences' lengths; no prompt fits in few rows.
   const int64_t rows = batch->tokens * a.group;
   if (rows <= kDecodeRows) return NVFP4_OK;
-  // Tensor map of the K codes as [(block, head)][token][value]: boxes of one head's rows, up to
-  // 128 bytes wide, in the layout of an MMA operand.
-  CUtensorMap k_map;
-  {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return NVFP4_ERR_CUDA;
-    const int D = cache->head_dim, B = cache->block_size, most = D == 256 ? 64 : 128;
-    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(B), cuuint64_t(cache->num_blocks * cache->n_kv_heads)};
-    cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(B) * D};
-    cuuint32_t box[3] = {cuuint32_t(D < 128 ? D : 128), cuuint32_t(B < most ? B : most), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cache->k, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return NVFP4_ERR_CUDA;
-  }
+  const int most = i == 2 ? attn::prompt::Cfg<256>::LOG_BOX : attn::prompt::Cfg<128>::LOG_BOX;
+  if (!encode_cache_map(&k_map, cache->k, cache, log_block < most ? log_block : most)) return NVFP4_ERR_CUDA;
   auto launch_prompt = [&](auto kernel, int tile_rows, int smem) {
     const int64_t items = (rows / tile_rows + batch->n_seqs) * a.kv_heads;
     if (items > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
