@@ -8,11 +8,12 @@
 // HBM-bound: 2 bytes read and 2 written per element.  A lane holds 8 consecutive values
 // (16 bytes), D / 8 lanes a head, a warp 256 / D heads at a time; sums and the halves of
 // a rotated pair travel by shuffles (the raw BF16 words of the partner lane: four
-// shuffles instead of eight).  A warp takes a run of one token's heads, so that the
-// table row and the norm weights are loaded once, with four heads' loads in flight.
+// shuffles instead of eight).  A warp takes a run of one token's heads and forms the products of
+// norm weight and rotation once, y = (x (w c) + x_partner (w_partner s)) / rms, which leaves three
+// packed FP32 operations per pair of values; kDepth heads' loads are in flight.
 #pragma once
 
-#include "ptx.cuh"
+#include "gdn.cuh"
 
 namespace nvfp4 {
 namespace headnorm {
@@ -38,13 +39,10 @@ struct Args {
   int per_part;               // head groups per warp
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &w, float2 (&f)[4]) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(x[i] << 16);
-    f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
 }
 
 template <int LANES>
@@ -60,46 +58,45 @@ __device__ __forceinline__ float group_max(float x) {
   return x;
 }
 
-// 1 / sqrt(mean(x^2) + eps) times 2^-e in `inv`, and 2^e's inverse already in x: squares
-// that leave FP32's range are taken of x scaled by a power of two instead.
+// 1 / sqrt(x) to 2 ulp, for normal x.
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <int D>
-__device__ __forceinline__ float inv_rms(float (&x)[8], float (&p)[8], float eps) {
-  constexpr int LANES = D / 8;
-  float ss = 0.0f;
+__device__ __forceinline__ float sum_squares(const float2 (&x)[4]) {
+  float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = group_sum<LANES>(ss);
-  const bool odd = ss > 1e37f || ss < 1e-30f;
-  if (__any_sync(0xffffffffu, odd)) {
-    float m = 0.0f;
+  for (int i = 0; i < 4; ++i) s = gdn::ffma2(x[i], x[i], s);
+  return group_sum<D / 8>(s.x + s.y);
+}
+
+// Whether a sum of squares left FP32's range, or lost bits below it that eps does not outweigh.
+__device__ __forceinline__ bool outside(float ss, float eps) { return !(ss <= 1e37f) || (ss < 1e-30f && eps < 1e-25f); }
+
+// 1 / sqrt(mean(x^2) + eps) of such a head: of x scaled by a power of two, by which x and its
+// partner's values p are then scaled too.
+template <int D>
+__device__ __forceinline__ float careful_inv_rms(float2 (&x)[4], float2 (&p)[4], float eps) {
+  float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-    m = group_max<LANES>(m);
-    // with an eps that outweighs them, tiny squares need no care
-    if (odd && m > 0.0f && m <= 3.4e38f && (m > 1.0f || eps < 1e-25f)) {
-      int e;
-      frexpf(m, &e);
-      e = max(e, -90);
-      const float f = ldexpf(1.0f, -e);
-      float s2 = 0.0f;
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+  m = group_max<D / 8>(m);
+  if (m > 0.0f && m <= 3.4e38f) {
+    int e;
+    frexpf(m, &e);
+    e = max(e, -90);
+    const float f = ldexpf(1.0f, -e);
+    eps = ldexpf(eps, -2 * e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= f;
-        p[i] *= f;
-        s2 = fmaf(x[i], x[i], s2);
-      }
-      ss = s2;
-      eps = ldexpf(eps, -2 * e);
-    } else if (odd) {
-      ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < 4; ++i) {
+      x[i] = gdn::fmul2(x[i], make_float2(f, f));
+      p[i] = gdn::fmul2(p[i], make_float2(f, f));
     }
-    // every lane takes part; a group that was fine sums to what it had
-    const float again = group_sum<LANES>(odd ? ss : 0.0f);
-    if (odd) ss = again;
   }
-  return 1.0f / sqrtf(ss * (1.0f / D) + eps);
+  return rsqrtf(sum_squares<D>(x) * (1.0f / D) + eps);
 }
 
 template <int D>
@@ -112,9 +109,10 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_consta
   const int part = static_cast<int>(wid - tok * a.parts);
   if (tok >= a.tokens) return;  // whole warps
   const int lane = threadIdx.x & 31, sub = lane / LANES, l = lane % LANES;
-  const int total = a.heads + a.kv_heads;
-  const int h_begin = part * a.per_part * HPW, h_end = min(total, h_begin + a.per_part * HPW);
-  if (h_begin >= total) return;
+  // head groups of this warp: [g_begin, g_end) of q's groups followed by k's
+  const int q_groups = (a.heads + HPW - 1) / HPW, groups = q_groups + (a.kv_heads + HPW - 1) / HPW;
+  const int g_begin = part * a.per_part, g_end = min(groups, g_begin + a.per_part);
+  if (g_begin >= groups) return;
 
   const int64_t pos = a.rot ? __ldg(a.positions + tok) : 0;
   if (pos < 0 || pos >= a.max_pos) {  // no such row in the table: the token is left alone
@@ -122,117 +120,112 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_consta
     return;
   }
 
-  // Rotation of the lane's 8 values: y = n * c + n_partner * s, with the sign in s.
-  float c[8], s[8];
+  // The lane's 8 values: y = (x * A + p * B) / rms with A = w c, B = w_partner s, the sign in s.
   const int first = 8 * l, half = a.rot / 2;
   const bool rotated = first < a.rot;
   int partner = lane;
-  if (rotated) {
+  if (rotated && !a.interleaved) partner = first >= half ? lane - half / 8 : lane + half / 8;
+  float2 A[4], B[4];
+  auto load_factors = [&](const uint16_t *src) {
+    float2 w[4], wp[4];
+    unpack8(__ldg(reinterpret_cast<const uint4 *>(src + first)), w);
+    unpack8(__ldg(reinterpret_cast<const uint4 *>(src + 8 * (partner % LANES))), wp);
+    const float2 off = make_float2(a.w_offset, a.w_offset);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      A[i] = add_f32x2(w[i], off);
+      wp[i] = add_f32x2(wp[i], off);
+      B[i] = make_float2(0.0f, 0.0f);
+    }
+    if (!rotated) return;
     const float *row = a.table + pos * a.rot;
-    if (a.interleaved) {
-      const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + first / 2));
-      const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + first / 2));
-      const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+    if (a.interleaved) {  // values 2 i and 2 i + 1 are a pair
+      const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + first / 2));
+      const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + first / 2));
+      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = c4[i];
-        s[2 * i] = -s4[i];
-        s[2 * i + 1] = s4[i];
+        B[i] = make_float2(A[i].y * -s[i], A[i].x * s[i]);
+        A[i] = make_float2(A[i].x * c[i], A[i].y * c[i]);
       }
     } else {
       const bool upper = first >= half;
-      const int at = upper ? first - half : first;
+      const float *at = row + (upper ? first - half : first);
+      const float sg = upper ? 1.0f : -1.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + at) + i);
-        const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + at) + i);
-        const float sg = upper ? 1.0f : -1.0f;
-        c[4 * i] = cc.x, c[4 * i + 1] = cc.y, c[4 * i + 2] = cc.z, c[4 * i + 3] = cc.w;
-        s[4 * i] = sg * ss.x, s[4 * i + 1] = sg * ss.y, s[4 * i + 2] = sg * ss.z, s[4 * i + 3] = sg * ss.w;
+      for (int i = 0; i < 4; ++i) {
+        const float2 c = __ldg(reinterpret_cast<const float2 *>(at) + i), s = __ldg(reinterpret_cast<const float2 *>(at + half) + i);
+        A[i] = gdn::fmul2(A[i], c);
+        B[i] = gdn::fmul2(wp[i], make_float2(sg * s.x, sg * s.y));
       }
-      partner = upper ? lane - half / 8 : lane + half / 8;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = 1.0f;
-      s[i] = 0.0f;
-    }
-  }
-  const int pl = 8 * (partner % LANES);  // the partner's first value
-
-  // The weights change once, between the last query head and the first key head.
-  float w[8], wp[8];
-  bool have_k = false;
-  auto load_weights = [&](const uint16_t *src) {
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(src + first)), w);
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(src + pl)), wp);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] += a.w_offset;
-      wp[i] += a.w_offset;
     }
   };
-  load_weights(h_begin + sub < a.heads ? a.w_q : a.w_k);
-  have_k = h_begin + sub >= a.heads;
-
-  for (int h0 = h_begin; h0 < h_end; h0 += kDepth * HPW) {
-    uint4 raw[kDepth];
+  auto expand = [&](const uint4 &raw, float2 (&x)[4], float2 (&p)[4]) {
+    unpack8(raw, x);
+    if (a.interleaved) {
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int h = h0 + u * HPW + sub;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (h < h_end) {
-        const uint16_t *src = h < a.heads ? a.q + tok * a.ld_q + int64_t(h) * D : a.k + tok * a.ld_k + int64_t(h - a.heads) * D;
-        raw[u] = *reinterpret_cast<const uint4 *>(src + first);  // q_out may be q itself: no read-only path
-      }
+      for (int i = 0; i < 4; ++i) p[i] = make_float2(x[i].y, x[i].x);
+    } else {
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, raw.x, partner);
+      o.y = __shfl_sync(0xffffffffu, raw.y, partner);
+      o.z = __shfl_sync(0xffffffffu, raw.z, partner);
+      o.w = __shfl_sync(0xffffffffu, raw.w, partner);
+      unpack8(o, p);
     }
+  };
+  auto store = [&](uint16_t *to, const float2 (&x)[4], const float2 (&p)[4], float inv) {
+    uint32_t out[4];
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      if (h0 + u * HPW >= h_end) break;  // uniform over the warp
-      const int h = h0 + u * HPW + sub;
-      float x[8], p[8];
-      unpack8(raw[u], x);
-      if (a.interleaved) {
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = gdn::fmul2(gdn::ffma2(x[i], A[i], gdn::fmul2(p[i], B[i])), make_float2(inv, inv));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+      out[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+  };
+  // Groups [g0, g1) of one operand: head g * HPW + sub of `heads`, rows `from` / `to` at the lane's values.
+  auto run = [&](const uint16_t *from, uint16_t *to, const uint16_t *w, int heads, int g0, int g1) {
+    if (g0 >= g1) return;
+    load_factors(w);
+    from += (g0 * HPW + sub) * D;
+    to += (g0 * HPW + sub) * D;
+    const int n = min(g1 * HPW, heads) - (g0 * HPW + sub);  // heads left, from this lane's first on
+    bool odd = false;  // some head's squares were outside FP32's range: it is left to the second pass
+#pragma unroll 1
+    for (int g = 0; g < g1 - g0; g += kDepth) {
+      const uint16_t *src = from + g * HPW * D;
+      uint16_t *dst = to + g * HPW * D;
+      uint4 raw[kDepth];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
-      } else {
-        uint4 o;
-        o.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
-        o.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
-        o.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
-        o.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
-        unpack8(o, p);
+      for (int u = 0; u < kDepth; ++u) {  // `to` may be `from`: no read-only path
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if ((g + u) * HPW < n) raw[u] = *reinterpret_cast<const uint4 *>(src + u * HPW * D);
       }
-      const float inv = inv_rms<D>(x, p, a.eps);
-      if (h >= a.heads && !have_k) {
-        load_weights(a.w_k);
-        have_k = true;
-      }
-      uint32_t out[4];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        float y[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float n = x[i + j] * inv * w[i + j];
-          if (rotated) {
-            const float np = p[i + j] * inv * (a.interleaved ? w[(i + j) ^ 1] : wp[i + j]);
-            y[j] = fmaf(n, c[i + j], np * s[i + j]);
-          } else {
-            y[j] = n;
-          }
+      for (int u = 0; u < kDepth; ++u) {
+        float2 x[4], p[4];
+        expand(raw[u], x, p);
+        const float ss = sum_squares<D>(x);
+        if ((g + u) * HPW < n) {
+          if (outside(ss, a.eps)) odd = true;
+          else store(dst + u * HPW * D, x, p, rsqrt_approx(ss * (1.0f / D) + a.eps));
         }
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y[0], y[1]);
-        out[i / 2] = *reinterpret_cast<const uint32_t *>(&b);
-      }
-      if (h < h_end) {
-        uint16_t *dst = h < a.heads ? a.q_out + tok * a.ld_qo + int64_t(h) * D
-                                    : a.k_out + tok * a.ld_ko + int64_t(h - a.heads) * D;
-        *reinterpret_cast<uint4 *>(dst + first) = make_uint4(out[0], out[1], out[2], out[3]);
       }
     }
-  }
+    if (!__any_sync(0xffffffffu, odd)) return;
+#pragma unroll 1
+    for (int g = 0; g < g1 - g0; ++g) {
+      const bool have = g * HPW < n;
+      float2 x[4], p[4];
+      expand(have ? *reinterpret_cast<const uint4 *>(from + g * HPW * D) : make_uint4(0, 0, 0, 0), x, p);
+      const bool again = have && outside(sum_squares<D>(x), a.eps);
+      const float inv = careful_inv_rms<D>(x, p, a.eps);
+      if (again) store(to + g * HPW * D, x, p, inv);
+    }
+  };
+  run(a.q + tok * a.ld_q + first, a.q_out + tok * a.ld_qo + first, a.w_q, a.heads, g_begin, min(g_end, q_groups));
+  run(a.k + tok * a.ld_k + first, a.k_out + tok * a.ld_ko + first, a.w_k, a.kv_heads, max(g_begin, q_groups) - q_groups, g_end - q_groups);
 }
 
 // table[p][i] = cos(p base^(-2i/R)), table[p][R/2 + i] = sin of the same, i < R/2.  FP64:

@@ -97,21 +97,31 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
 
   const int pieces = (end - held) << log_c;
   uint4 x[CHUNKS];
-  uint32_t m = 0;  // largest finite magnitude, as BF16 bits
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
     const int p = tid + i * THREADS;
     x[i] = make_uint4(0, 0, 0, 0);
     if (p < pieces) x[i] = __ldg(reinterpret_cast<const uint4 *>(src + (p >> log_c) * ld + ((p & ((1 << log_c) - 1)) << 3)));
   }
+  // largest finite magnitude: BF16 magnitudes order as integers, two at a time
+  uint32_t m2 = 0;
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    m2 = __vmaxu2(__vmaxu2(m2, x[i].x & 0x7fff7fffu), x[i].y & 0x7fff7fffu);
+    m2 = __vmaxu2(__vmaxu2(m2, x[i].z & 0x7fff7fffu), x[i].w & 0x7fff7fffu);
+  }
+  uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  if (m >= 0x7f80u) {  // an infinity or NaN does not set the scale
+    m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t u0 = w[j] & 0x7fffu, u1 = (w[j] >> 16) & 0x7fffu;
-      if (u0 < 0x7f80u) m = max(m, u0);  // an infinity or NaN does not set the scale
-      if (u1 < 0x7f80u) m = max(m, u1);
+    for (int i = 0; i < CHUNKS; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t u0 = w[j] & 0x7fffu, u1 = (w[j] >> 16) & 0x7fffu;
+        if (u0 < 0x7f80u) m = max(m, u0);
+        if (u1 < 0x7f80u) m = max(m, u1);
+      }
     }
   }
   m = __reduce_max_sync(0xffffffffu, m);

@@ -1012,7 +1012,7 @@ nvfp4_status_t nvfp4_qk_norm_rope(const void *q_bf16, int64_t ld_q, const void *
   // Few tokens: a warp takes one head group, so that all SMs have work; many: whole
   // tokens, so that the table row and weights are read once.
   const int per_warp = 32 / (head_dim / 8);
-  const int groups = (n_heads + n_kv_heads + per_warp - 1) / per_warp;
+  const int groups = (n_heads + per_warp - 1) / per_warp + (n_kv_heads + per_warp - 1) / per_warp;
   const int64_t warps = int64_t(dev->sms) * 32;
   int64_t parts = tokens >= warps ? 1 : (warps + tokens - 1) / tokens;
   if (parts > groups) parts = groups;
