@@ -514,7 +514,7 @@ NVFP4_API nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n
  *   The products of codes and block scales are exact in FP16; x is scaled by a power of two
  *   per 1024 columns and keeps its BF16 bits down to 2^-29 of their largest; FP32 sums.
  *   x: device BF16 [M x ld_x], 16-byte aligned, ld_x % 8 == 0.  W: as in nvfp4_linear, with
- *   K % 64 == 0, codes 32-byte aligned, any number of rows.  segs: as in nvfp4_linear, with
+ *   K % 64 == 0 and any number of rows.  segs: as in nvfp4_linear, with
  *   no alignment of their bounds.  out: BF16 or FP32 per out_kind, ldo >= N, any ldo.
  */
 NVFP4_API nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const nvfp4_operand_t *W,

@@ -6,13 +6,16 @@
 // which keeps all BF16 bits within 2^-29 of the chunk's largest value.  FP32 sums.
 //
 // Bound by HBM: 9/16 byte per weight, read once.  A CTA takes 128 weight rows (one atom row
-// of the scale layout) and a K range; a lane reads 32 bytes of two rows per step, 64
-// consecutive columns, with their four scales in one word.  The contraction runs over
-// columns in any order as long as W and x agree, so those 64 columns are the lane's values
-// of 16 k-steps and need no shuffling.  The rows of a warp are 4 w + i + 32 j (i, j < 4): their
-// scale words fill whole 16-byte pieces.  x is converted once per CTA and chunk, into
-// shared memory.  When the row blocks alone do not fill the GPU, a cluster of CTAs splits K
-// and adds its partial sums through distributed shared memory, in rank order.
+// of the scale layout) and a K range, which a producer warp streams through a ring of stages
+// of 256 columns (16 KB of codes by TMA, 2 KB of scales), so that up to 144 KB are on their way to an
+// SM.  A lane reads 32 bytes, 64 consecutive columns, of two rows per stage, with their four scales in
+// one word.  The contraction runs over columns in any order as long as W and x agree, so
+// those 64 columns are the lane's values of 16 k-steps and need no shuffling.  The rows of a
+// warp are 4 w + i + 32 j (i, j < 4), as the scale layout groups them; with the TMA's swizzle the
+// reads of codes are free of bank conflicts.  x is converted once per CTA and chunk, into
+// shared memory, the next chunk's loads in flight meanwhile.  When the row blocks alone do not
+// fill the GPU, a cluster of CTAs splits K and adds its partial sums through distributed shared
+// memory, in rank order.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -21,19 +24,20 @@
 namespace nvfp4 {
 namespace matvec {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                   // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
 constexpr int kBN = 128;      // weight rows per CTA
 constexpr int kChunk = 1024;  // columns of x staged at a time
-constexpr int kStep = 256;    // columns of a warp's step
+constexpr int kStep = 256;    // columns of a stage
+constexpr int kCodeBytes = kBN * kStep / 2, kScaleBytes = kBN * kStep / 16;
 
 struct Args {
   const uint16_t *x;  // BF16 [M x ld_x]
   int64_t ld_x;
   int M;
-  const uint8_t *codes, *scales;
+  const uint8_t *scales;
   int64_t N, K;
-  int64_t k_per_cta;  // multiple of kChunk
+  int64_t k_per_cta;  // multiple of kStep
   int nseg;
   gemm::Segment seg[16];
   void *out;
@@ -41,14 +45,16 @@ struct Args {
   int out_fp32;
 };
 
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b, z0, z1, z2;\n\t"
-      "mov.b32 {b, z0, z1, z2}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-      : "=r"(r)
-      : "r"(byte));
-  return r;
+// Eight codes of a word as four FP16 pairs.
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -56,175 +62,203 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// 32 bytes through one load.
-struct W32 {
-  uint32_t w[8];
-};
-__device__ __forceinline__ W32 ld_w32(const uint8_t *p) {
-  W32 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
-                 "=r"(r.w[7])
-               : "l"(p));
-  return r;
-}
-
 template <int NB>
 struct Smem {
+  static constexpr int kStages = NB == 1 ? 4 : 3;  // two CTAs fit an SM
+  alignas(1024) unsigned char codes[kStages][kCodeBytes];
+  alignas(128) unsigned char scales[kStages][kScaleBytes];
   // x chunk as FP16, token rows; the 16-byte pieces of lane q's 64 columns are permuted so
   // that the eight lanes of a quarter-warp hit distinct banks
   alignas(128) uint16_t x[8 * NB][kChunk];
   float scale[8 * NB];           // 2^e of each token's chunk
   float acc[kBN][8 * NB + 1];
+  uint64_t full[kStages], empty[kStages];
 };
+template <int NB>
+constexpr int smem_bytes() {
+  return 1024 + int(sizeof(Smem<NB>));
+}
 
 // 16-byte piece p of a token's chunk.
 __device__ __forceinline__ int piece(int tok, int p) {
   return (p & ~7) | ((p & 7) ^ (((p >> 3) & 3) | (tok & 1) << 2));
 }
 
+// One warp's tokens of an x chunk: loads, then conversion into shared memory.
+template <int NB>
+struct XChunk {
+  static constexpr int T = NB;  // tokens per warp
+  uint4 raw[T][4];
+
+  __device__ __forceinline__ void load(const Args &a, int warp, int lane, int64_t k0, int64_t k_end) {
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+      const int t = warp + kWarps * u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t k = k0 + 8 * (lane + 32 * i);
+        raw[u][i] = t < a.M && k < k_end ? __ldg(reinterpret_cast<const uint4 *>(a.x + t * a.ld_x + k)) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(Smem<NB> &sm, int warp, int lane) const {
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+      const int t = warp + kWarps * u;
+      uint32_t top = 0;  // BF16 magnitudes order as integers, two at a time
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        top = __vmaxu2(__vmaxu2(top, raw[u][i].x & 0x7fff7fffu), raw[u][i].y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, raw[u][i].z & 0x7fff7fffu), raw[u][i].w & 0x7fff7fffu);
+      }
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)) << 16;
+      // 2^-e brings the chunk's largest magnitude into [2^14, 2^15); an infinity counts as the
+      // largest finite value, so that finite values stay finite next to it
+      const int e = bits == 0 ? 0 : min(max(static_cast<int>(bits >> 23) - 127 - 14, -126), 113);
+      const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      if (lane == 0) sm.scale[t] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v[4] = {raw[u][i].x, raw[u][i].y, raw[u][i].z, raw[u][i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = attn::pack_f16(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xFFFF0000u) * f);
+        *reinterpret_cast<uint4 *>(&sm.x[t][8 * piece(t, lane + 32 * i)]) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+};
+
 // Grid: (row blocks * cluster size), cluster of CTAs along K.  NB: blocks of 8 tokens.
 template <int NB>
-__global__ void __launch_bounds__(kThreads) matvec_kernel(const __grid_constant__ Args a) {
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  Smem<NB> &sm = *reinterpret_cast<Smem<NB> *>(smem_raw);
-  grid_dep_wait();
-  grid_dep_launch();
+__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map) {
+  constexpr int kStages = Smem<NB>::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  Smem<NB> &sm = *reinterpret_cast<Smem<NB> *>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   uint32_t nrank, rank = cluster_ctarank();
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nrank));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int64_t n0 = int64_t(blockIdx.x / nrank) * kBN;
   const int64_t k_begin = rank * a.k_per_cta, k_end = min(a.K, k_begin + a.k_per_cta);
-
-  // this lane's two weight rows: mma rows g and g + 8
-  int64_t row[2];
-  const uint8_t *wp[2], *sp[2];
-  const int64_t kb_atoms = a.K / 64;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int local = 4 * warp + (g & 3) + 32 * ((g >> 2) + 2 * r);
-    row[r] = n0 + local;
-    wp[r] = a.codes + row[r] * (a.K / 2) + 32 * q;
-    sp[r] = a.scales + scale_word_offset(row[r], q, kb_atoms);
+  const int steps = k_end > k_begin ? static_cast<int>((k_end - k_begin + kStep - 1) / kStep) : 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kWarps);
+    }
+    fence_barrier_init();
   }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+
+  bool ok = true;
   float acc[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[b][j] = 0.0f;
 
-  auto load_step = [&](int64_t k, W32 (&w)[2], uint32_t (&s)[2]) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool ok = row[r] < a.N && k + 64 * q < k_end;
-      s[r] = ok ? __ldg(reinterpret_cast<const uint32_t *>(sp[r] + (k / 64) * 512)) : 0u;
-      if (ok) {
-        w[r] = ld_w32(wp[r] + k / 2);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[r].w[i] = 0;
+  if (warp == kWarps) {
+    if (lane == 0) {
+      const int64_t atoms = a.K / 64;
+      const uint8_t *sf = a.scales + (n0 / 128) * atoms * 512;
+      for (int i = 0; i < steps && ok; ++i) {
+        const int st = i % kStages;
+        ok = mbar_wait(&sm.empty[st], ((i / kStages) & 1) ^ 1);
+        if (!ok) break;
+        const int64_t k = k_begin + int64_t(i) * kStep;
+        const uint32_t bytes = static_cast<uint32_t>(min(int64_t(4), atoms - k / 64)) * 512;
+        mbar_arrive_expect_tx(&sm.full[st], kCodeBytes + bytes);
+        tma_load_2d(sm.codes[st], &map, &sm.full[st], static_cast<int>(k / 2), static_cast<int>(n0));  // zeros outside W
+        bulk_load(sm.scales[st], sf + (k / 64) * 512, bytes, &sm.full[st]);
       }
     }
-  };
-
-  W32 w[2];
-  uint32_t s[2];
-  load_step(k_begin, w, s);
-  for (int64_t k0 = k_begin; k0 < k_end; k0 += kChunk) {
-    // stage x: a warp takes whole tokens, 32 columns a lane
-    for (int t = warp; t < 8 * NB; t += kWarps) {
-      uint4 raw[4];
-      float amax = 0.0f;
+  } else {
+    // this lane's two weight rows: mma rows g and g + 8
+    int row[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t k = k0 + 8 * (lane + 32 * i);
-        raw[i] = t < a.M && k < k_end ? __ldg(reinterpret_cast<const uint4 *>(a.x + t * a.ld_x + k)) : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    for (int r = 0; r < 2; ++r) row[r] = 4 * warp + (g & 3) + 32 * ((g >> 2) + 2 * r);
+    const bool have[2] = {n0 + row[0] < a.N, n0 + row[1] < a.N};
+    XChunk<NB> x;
+    x.load(a, warp, lane, k_begin, k_end);
+    constexpr int kPerChunk = kChunk / kStep;
+    for (int i0 = 0; i0 < steps; i0 += kPerChunk) {  // to the end even if a wait ran out: others wait here
+      x.store(sm, warp, lane);
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // consumer warps
+      if (i0 + kPerChunk < steps) x.load(a, warp, lane, k_begin + int64_t(i0 + kPerChunk) * kStep, k_end);
+      float c[NB][2][4];  // two chains: even and odd k-steps
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[j] << 16)), fabsf(__uint_as_float(v[j] & 0xFFFF0000u))));
-      }
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = attn::row_exponent(amax);
-      const float f0 = ldexpf(1.0f, -(e / 2)), f1 = ldexpf(1.0f, -(e - e / 2));
-      if (lane == 0) sm.scale[t] = ldexpf(1.0f, e);
+        for (int j = 0; j < 8; ++j) c[b][j >> 2][j & 3] = 0.0f;
+#pragma unroll 1
+      for (int s = 0; s < kPerChunk && i0 + s < steps; ++s) {
+        const int i = i0 + s, st = i % kStages;
+        ok = ok && mbar_wait(&sm.full[st], (i / kStages) & 1);
+        const bool inside = k_begin + int64_t(i) * kStep + 64 * q < k_end;
+        uint32_t w[2][8], sc[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = attn::pack_f16(__uint_as_float(v[j] << 16) * f0 * f1, __uint_as_float(v[j] & 0xFFFF0000u) * f0 * f1);
-        *reinterpret_cast<uint4 *>(&sm.x[t][8 * piece(t, lane + 32 * i)]) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    }
-    __syncthreads();
-    float c[NB][2][4];  // two chains: even and odd k-steps
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[b][j >> 2][j & 3] = 0.0f;
-#pragma unroll
-    for (int st = 0; st < kChunk / kStep; ++st) {
-      const int64_t k = k0 + st * kStep;
-      if (k >= k_end) break;
-      W32 nw[2];
-      uint32_t ns[2];
-      load_step(k + kStep, nw, ns);  // next step, possibly of the next chunk
-      uint32_t sc[2][4];  // the four scales of each row, twice each
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t lo = attn::e4m3x2_to_f16x2(s[r]), hi = attn::e4m3x2_to_f16x2(s[r] >> 16);
-        sc[r][0] = __byte_perm(lo, lo, 0x1010);
-        sc[r][1] = __byte_perm(lo, lo, 0x3232);
-        sc[r][2] = __byte_perm(hi, hi, 0x1010);
-        sc[r][3] = __byte_perm(hi, hi, 0x3232);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // word i: k-steps 2 i, 2 i + 1, group i / 2
-        uint4 xb[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          xb[b] = *reinterpret_cast<const uint4 *>(&sm.x[8 * b + g][8 * piece(g, st * 32 + q * 8 + i)]);
-        uint32_t v[2][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[r][j] = mul_f16x2(e2m1x2_to_f16x2(w[r].w[i] >> (8 * j)), sc[r][i >> 1]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          attn::mma_f16(c[b][0], v[0][0], v[1][0], v[0][1], v[1][1], xb[b].x, xb[b].y);
-          attn::mma_f16(c[b][1], v[0][2], v[1][2], v[0][3], v[1][3], xb[b].z, xb[b].w);
+        for (int r = 0; r < 2; ++r) {
+          const unsigned char *src = sm.codes[st] + row[r] * 128;
+          const uint4 lo = *reinterpret_cast<const uint4 *>(src + (((2 * q) ^ (row[r] & 7)) << 4));
+          const uint4 hi = *reinterpret_cast<const uint4 *>(src + (((2 * q + 1) ^ (row[r] & 7)) << 4));
+          w[r][0] = lo.x, w[r][1] = lo.y, w[r][2] = lo.z, w[r][3] = lo.w;
+          w[r][4] = hi.x, w[r][5] = hi.y, w[r][6] = hi.z, w[r][7] = hi.w;
+          uint32_t f = *reinterpret_cast<const uint32_t *>(sm.scales[st] + 512 * q + (row[r] & 31) * 16 + (row[r] >> 5) * 4);
+          if (!(have[r] && inside)) f = 0;  // padding's scales may be anything
+          uint32_t a0, a1;
+          attn::e4m3x4_to_f16x4(f, a0, a1);
+          sc[r][0] = __byte_perm(a0, a0, 0x1010);
+          sc[r][1] = __byte_perm(a0, a0, 0x3232);
+          sc[r][2] = __byte_perm(a1, a1, 0x1010);
+          sc[r][3] = __byte_perm(a1, a1, 0x3232);
         }
-      }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        w[r] = nw[r];
-        s[r] = ns[r];
+        for (int n = 0; n < 8; ++n) {  // word n: k-steps 2 n, 2 n + 1, group n / 2
+          uint4 xb[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            xb[b] = *reinterpret_cast<const uint4 *>(&sm.x[8 * b + g][8 * piece(g, s * 32 + q * 8 + n)]);
+          uint32_t v[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            e2m1x8_to_f16x8(w[r][n], v[r]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[r][j] = mul_f16x2(v[r][j], sc[r][n >> 1]);
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            attn::mma_f16(c[b][0], v[0][0], v[1][0], v[0][1], v[1][1], xb[b].x, xb[b].y);
+            attn::mma_f16(c[b][1], v[0][2], v[1][2], v[0][3], v[1][3], xb[b].z, xb[b].w);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[st]);
       }
+      // accumulator j: row g + 8 (j / 2), token 2 q + j % 2
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[b][j] = fmaf(c[b][0][j] + c[b][1][j], sm.scale[8 * b + 2 * q + (j & 1)], acc[b][j]);
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // x is staged again
     }
-    // accumulator j: row g + 8 (j / 2), token 2 q + j % 2
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[b][j] = fmaf(c[b][0][j] + c[b][1][j], sm.scale[8 * b + 2 * q + (j & 1)], acc[b][j]);
-    __syncthreads();  // x is staged again
+        sm.acc[row[j >> 1]][8 * b + 2 * q + (j & 1)] = acc[b][j];
   }
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      sm.acc[4 * warp + (g & 3) + 32 * ((g >> 2) + 2 * (j >> 1))][8 * b + 2 * q + (j & 1)] = acc[b][j];
+  __syncwarp();
   cluster_sync();
 
-  // rank r adds rows [r, r + 1) * 128 / nrank of all the cluster's partial sums
-  const int per = kBN / nrank;
+  // rank r adds its share of the rows of all the cluster's partial sums
+  const int per = (kBN + nrank - 1) / nrank;
   for (int idx = threadIdx.x; idx < per * a.M; idx += kThreads) {
     const int t = idx / per, local = static_cast<int>(rank) * per + idx % per;
     const int64_t n = n0 + local;
-    if (n >= a.N) continue;
+    if (local >= kBN || n >= a.N) continue;
     float y = 0.0f;
     for (uint32_t r = 0; r < nrank; ++r) {
       float v;

@@ -82,6 +82,10 @@ nvfp4_status_t current_device(DeviceInfo **info) {
                              int(sizeof(gdn::Smem<32>))) != cudaSuccess ||
         cudaFuncSetAttribute(gdn::recurrence_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(sizeof(gdn::Smem<16>))) != cudaSuccess ||
+        cudaFuncSetAttribute(matvec::matvec_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             matvec::smem_bytes<1>()) != cudaSuccess ||
+        cudaFuncSetAttribute(matvec::matvec_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             matvec::smem_bytes<2>()) != cudaSuccess ||
         cudaFuncSetAttribute(attn::decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              attn::decode_smem_bytes<64>()) != cudaSuccess ||
         cudaFuncSetAttribute(attn::decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1182,7 +1186,7 @@ nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const n
     expect = segs[i].n_end;
   }
   if (expect != N) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned(x_bf16, 16) || ld_x % 8 != 0 || !aligned(W->codes, 32) || !aligned(W->scales, 16) ||
+  if (!aligned(x_bf16, 16) || ld_x % 8 != 0 || !aligned(W->codes, 16) || !aligned(W->scales, 16) ||
       !aligned(out, out_kind == NVFP4_OUT_BF16 ? 2 : 4))
     return NVFP4_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
@@ -1190,7 +1194,6 @@ nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const n
   a.x = static_cast<const uint16_t *>(x_bf16);
   a.ld_x = ld_x;
   a.M = static_cast<int>(M);
-  a.codes = W->codes;
   a.scales = W->scales;
   a.N = N;
   a.K = K;
@@ -1199,16 +1202,22 @@ nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const n
   a.ldo = ldo;
   a.out_fp32 = out_kind == NVFP4_OUT_F32;
   const int64_t blocks = (N + matvec::kBN - 1) / matvec::kBN;
-  const int64_t chunks = (K + matvec::kChunk - 1) / matvec::kChunk;
-  int cluster = 1;
-  while (cluster < 8 && cluster * 2 <= chunks && blocks * cluster < 2 * dev->sms) cluster *= 2;
-  a.k_per_cta = (chunks + cluster - 1) / cluster * matvec::kChunk;
+  // K split over a cluster of up to 8 CTAs, as many as find a place at once (two per SM), then as
+  // few as have the same number of steps each.
+  const int64_t steps = (K + matvec::kStep - 1) / matvec::kStep;
+  int64_t most = 2 * dev->sms / blocks;
+  most = most < 1 ? 1 : most > 8 ? 8 : most;
+  const int64_t each = (steps + most - 1) / most;
+  const int cluster = static_cast<int>((steps + each - 1) / each);
+  a.k_per_cta = (steps + cluster - 1) / cluster * matvec::kStep;
   if (blocks * cluster > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  CUtensorMap map;
+  if (!encode_codes_map(&map, W->codes, N, K, matvec::kBN)) return NVFP4_ERR_CUDA;
   const dim3 grid(static_cast<unsigned>(blocks * cluster));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (M <= 8)
-    return launch_pdl(matvec::matvec_kernel<1>, grid, dim3(matvec::kThreads), sizeof(matvec::Smem<1>), s, cluster, a);
-  return launch_pdl(matvec::matvec_kernel<2>, grid, dim3(matvec::kThreads), sizeof(matvec::Smem<2>), s, cluster, a);
+    return launch_pdl(matvec::matvec_kernel<1>, grid, dim3(matvec::kThreads), matvec::smem_bytes<1>(), s, cluster, a, map);
+  return launch_pdl(matvec::matvec_kernel<2>, grid, dim3(matvec::kThreads), matvec::smem_bytes<2>(), s, cluster, a, map);
 }
 
 nvfp4_status_t nvfp4_selftest_stalled_linear(const nvfp4_operand_t *A, const float *gs_a, const nvfp4_operand_t *W,

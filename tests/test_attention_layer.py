@@ -97,7 +97,7 @@ def test_matvec_refusals(L):
     assert call(M=17) == 2 and call(K=480, ld_x=480) == 2
     assert call(ld_x=504) == 1 and call(ldo=63) == 1
     assert call(segs=((0, 32, P),)) == 1 and call(segs=((0, 32, P), (40, 64, P))) == 1 and call(segs=((0, 64, None),)) == 1
-    assert call(x=P + 8) == 3 and call(codes=P + 16) == 3 and call(ld_x=516) == 3 and call(out=P + 1) == 3
+    assert call(x=P + 8) == 3 and call(codes=P + 8) == 3 and call(ld_x=516) == 3 and call(out=P + 1) == 3
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():
