@@ -494,14 +494,26 @@ def block_kv_cache(num_blocks: int, n_kv_heads: int, block_size: int, head_dim: 
     return BlockKVCache(k, v, ks, vs)
 
 
+# torch's types and the raw calls behind torch.cuda.current_stream / current_device, looked up
+# once: the calls below take microseconds on the GPU, and a serving step makes hundreds.
+_BF16 = _F32 = _U8 = _I32 = _I64 = _raw_stream = _current_device = None
+
+
+def _bind_torch():
+    global _BF16, _F32, _U8, _I32, _I64, _raw_stream, _current_device
+    import torch
+    _BF16, _F32, _U8, _I32, _I64 = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.int64
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _rows(x, name: str, dtype, dev: int = -1) -> int:
     """Checks a matrix argument (CUDA, 2-D, unit column stride) and returns its row stride."""
     shape, stride, at = x.shape, x.stride(), x.get_device()
     if at < 0 or x.dtype != dtype or len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor")
-    if shape[1] > 1 and stride[1] != 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if dev >= 0 and at != dev:
+    if at != dev and dev >= 0:
         raise ValueError(f"{name} is on another device")
     return stride[0] if shape[0] > 1 else shape[1]
 
@@ -510,64 +522,60 @@ def _launch(what: str, fn, dev: int, stream, made, *args):
     """Calls an entry point with its device current, on ``stream`` (default: the device's
     current one).  ``made``: buffers allocated by the caller, which the allocator has to
     know of when another stream than the current one uses them."""
-    import torch
-    raw = torch._C._cuda_getCurrentRawStream(dev)
+    raw = _raw_stream(dev)
     if stream is not None and stream.cuda_stream != raw:
         if stream.device.index != dev:
             raise ValueError("stream is on another device")
         for t in made:
-            t.record_stream(stream)
+            if t is not None:
+                t.record_stream(stream)
         raw = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         status = fn(*args, raw)
     else:
+        import torch
         with torch.cuda.device(dev):
             status = fn(*args, raw)
     if status != 0:
         raise NVFP4Error(status, what)
 
 
-def _out_buffer(like, shape, out, out_dtype: str, made):
-    """(out, kind, row stride) of a BF16 or FP32 result of ``shape``, allocated when None."""
-    import torch
+def _out_buffer(like, shape, out, out_dtype: str):
+    """(out, kind, row stride, out if it was allocated here) of a BF16 or FP32 result of ``shape``."""
     if out_dtype == "bf16":
-        dtype, kind = torch.bfloat16, 0
+        dtype, kind = _BF16, 0
     elif out_dtype == "f32":
-        dtype, kind = torch.float32, 1
+        dtype, kind = _F32, 1
     else:
         raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
     if out is None:
-        out = like.new_empty(shape, dtype=dtype)
-        made.append(out)
-        return out, kind, shape[1]
+        out = like.new_empty(shape) if kind == 0 else like.new_empty(shape, dtype=dtype)
+        return out, kind, shape[1], out
     ld = _rows(out, "out", dtype, like.get_device())
     if out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}")
-    return out, kind, ld
+    return out, kind, ld, None
 
 
 def _cache_struct(cache: BlockKVCache, dev: int) -> BlockCache:
-    import torch
     k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
-    shape, u8, f32 = k.shape, torch.uint8, torch.float32
-    if len(shape) != 4 or k.dtype != u8 or v.dtype != u8 or v.shape != shape:
+    shape = k.shape
+    if len(shape) != 4 or k.dtype != _U8 or v.dtype != _U8 or v.shape != shape:
         raise ValueError("cache k / v must be uint8 [num_blocks, n_kv_heads, block_size, head_dim]")
-    if ks.dtype != f32 or vs.dtype != f32 or ks.shape != shape[:2] or vs.shape != shape[:2]:
+    nb, hk, block, d = shape
+    if ks.dtype != _F32 or vs.dtype != _F32 or ks.shape != (nb, hk) or vs.shape != (nb, hk):
         raise ValueError("cache scales must be float32 [num_blocks, n_kv_heads]")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("cache tensors must be contiguous")
     if not k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == dev:
         raise ValueError("cache is on another device")
-    nb, hk, block, d = shape
     return BlockCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), nb, block, hk, d)
 
 
 def _batch_struct(cu_seqlens, kv_lens, block_table, tokens: int, dev: int) -> Batch:
-    import torch
-    i32 = torch.int32
-    ld = _rows(block_table, "block_table", i32, dev)
+    ld = _rows(block_table, "block_table", _I32, dev)
     n, cols = block_table.shape
-    if cu_seqlens.dtype != i32 or kv_lens.dtype != i32 or cu_seqlens.shape != (n + 1,) or kv_lens.shape != (n,):
+    if cu_seqlens.dtype != _I32 or kv_lens.dtype != _I32 or cu_seqlens.shape != (n + 1,) or kv_lens.shape != (n,):
         raise ValueError("cu_seqlens must be int32 [n_seqs + 1] and kv_lens int32 [n_seqs], n_seqs the rows of block_table")
     if not (cu_seqlens.is_contiguous() and kv_lens.is_contiguous()):
         raise ValueError("cu_seqlens and kv_lens must be contiguous")
@@ -580,6 +588,8 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     """FP32 [max_positions, rot_dim] table of cosines and sines for ``qk_norm_rope``, angles
     p * base^(-2i / rot_dim) computed in FP64."""
     import torch
+    if _BF16 is None:
+        _bind_torch()
     table = torch.empty((max_positions, rot_dim), dtype=torch.float32, device=device)
     _launch("nvfp4_rope_table", lib().nvfp4_rope_table, table.get_device(), stream, (table,), table.data_ptr(),
             max_positions, rot_dim, float(base))
@@ -595,8 +605,9 @@ def qk_norm_rope(q, k, w_q, w_k, positions=None, table=None, *, eps: float = 1e-
     ``weight_offset + w``; positions: int64 [tokens]; table: FP32 [max_positions, rot_dim]
     (``rope_table``), None for no rotation.  ``q_out`` / ``k_out`` may be ``q`` / ``k``.
     Returns ``(q_out, k_out)``."""
-    import torch
-    bf16 = torch.bfloat16
+    if _BF16 is None:
+        _bind_torch()
+    bf16 = _BF16
     ld_q, dev = _rows(q, "q", bf16), q.get_device()
     ld_k = _rows(k, "k", bf16, dev)
     tokens, width_q = q.shape
@@ -608,28 +619,28 @@ def qk_norm_rope(q, k, w_q, w_k, positions=None, table=None, *, eps: float = 1e-
         raise ValueError("q and k must have the same rows, of whole heads")
     rot = most = p_pos = p_table = 0
     if table is not None:
-        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.get_device() != dev:
+        if table.dtype != _F32 or table.dim() != 2 or not table.is_contiguous() or table.get_device() != dev:
             raise ValueError("table must be a contiguous float32 [max_positions, rot_dim] tensor on q's device")
-        if (positions is None or positions.dtype != torch.int64 or positions.shape != (tokens,)
+        if (positions is None or positions.dtype != _I64 or positions.shape != (tokens,)
                 or not positions.is_contiguous() or positions.get_device() != dev):
             raise ValueError("positions must be a contiguous int64 [tokens] tensor on q's device")
         most, rot = table.shape
         p_pos, p_table = positions.data_ptr(), table.data_ptr()
-    made = []
+    made_q = made_k = None
     if q_out is None:
-        q_out, ld_qo = q.new_empty((tokens, width_q)), width_q
-        made.append(q_out)
+        q_out = made_q = q.new_empty((tokens, width_q))
+        ld_qo = width_q
     else:
         ld_qo = _rows(q_out, "q_out", bf16, dev)
     if k_out is None:
-        k_out, ld_ko = q.new_empty((tokens, width_k)), width_k
-        made.append(k_out)
+        k_out = made_k = q.new_empty((tokens, width_k))
+        ld_ko = width_k
     else:
         ld_ko = _rows(k_out, "k_out", bf16, dev)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    if (made_q is None and q_out.shape != q.shape) or (made_k is None and k_out.shape != k.shape):
         raise ValueError("q_out / k_out must have the shape of q / k")
     if tokens:
-        _launch("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, dev, stream, made, q.data_ptr(), ld_q, k.data_ptr(),
+        _launch("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, dev, stream, (made_q, made_k), q.data_ptr(), ld_q, k.data_ptr(),
                 ld_k, tokens, width_q // d, width_k // d, d, w_q.data_ptr(), w_k.data_ptr(), weight_offset, eps,
                 p_pos, p_table, most, rot, interleaved, q_out.data_ptr(), ld_qo, k_out.data_ptr(), ld_ko)
     return q_out, k_out
@@ -639,9 +650,10 @@ def kv_append(k, v, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, strea
     """Quantise the new tokens' K and V rows (BF16 [tokens, n_kv_heads * head_dim]) into the
     cache.  Sequence s has the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1, the last of its
     kv_lens[s] tokens (int32 tensors); block_table: int32 [n_seqs, max_blocks]."""
-    import torch
-    ld_k, dev = _rows(k, "k", torch.bfloat16), k.get_device()
-    ld_v = _rows(v, "v", torch.bfloat16, dev)
+    if _BF16 is None:
+        _bind_torch()
+    ld_k, dev = _rows(k, "k", _BF16), k.get_device()
+    ld_v = _rows(v, "v", _BF16, dev)
     tokens, width = k.shape
     c = _cache_struct(cache, dev)
     if v.shape != k.shape or width != c.n_kv_heads * c.head_dim:
@@ -663,26 +675,25 @@ def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softm
     softmax_scale: default head_dim ** -0.5.  workspace: a contiguous CUDA tensor of at
     least ``attention_workspace_bytes(...)`` bytes (allocated here when None); calls that
     share one must not overlap on the GPU.  Returns out [tokens, heads * head_dim]."""
-    import torch
-    ld_q, dev = _rows(q, "q", torch.bfloat16), q.get_device()
+    if _BF16 is None:
+        _bind_torch()
+    ld_q, dev = _rows(q, "q", _BF16), q.get_device()
     tokens, width = q.shape
     c = _cache_struct(cache, dev)
     d = c.head_dim
     if d == 0 or width % d:
         raise ValueError("q must be [tokens, heads * head_dim] of the cache")
     b = _batch_struct(cu_seqlens, kv_lens, block_table, tokens, dev)
-    made = []
-    out, kind, ld_out = _out_buffer(q, q.shape, out, out_dtype, made)
+    out, kind, ld_out, made = _out_buffer(q, q.shape, out, out_dtype)
     if tokens == 0 or b.n_seqs == 0:
         return out
-    L = lib()
+    L, made_ws = lib(), None
     if workspace is None:
         need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, width // d, c.n_kv_heads, d)
-        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
-        made.append(workspace)
+        workspace = made_ws = q.new_empty(max(need, 16), dtype=_U8)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous, on q's device")
-    _launch("nvfp4_attention", L.nvfp4_attention, dev, stream, made, q.data_ptr(), ld_q, width // d, b, c,
+    _launch("nvfp4_attention", L.nvfp4_attention, dev, stream, (made, made_ws), q.data_ptr(), ld_q, width // d, b, c,
             d ** -0.5 if softmax_scale is None else softmax_scale, causal, out.data_ptr(), kind, ld_out,
             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
@@ -692,22 +703,23 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
     """x @ W^T for 1 to 16 token rows x (BF16 [tokens, K], not quantised) and an NVFP4
     weight.  segments: list of ``(n_begin, n_end, gs_w)``; default one with ``w.gs``.
     Returns out [tokens, N] (BF16 or FP32)."""
-    import torch
-    ld_x, dev = _rows(x, "x", torch.bfloat16), x.get_device()
+    if _BF16 is None:
+        _bind_torch()
+    ld_x, dev = _rows(x, "x", _BF16), x.get_device()
     codes, scales, rows, cols = w.codes, w.scales, w.rows, w.cols
     if x.shape[1] != cols:
         raise ValueError("x must have the weight's columns")
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError("the weight is on another device")
-    made = []
-    out, kind, ldo = _out_buffer(x, (x.shape[0], rows), out, out_dtype, made)
+    out, kind, ldo, made = _out_buffer(x, (x.shape[0], rows), out, out_dtype)
     if segments is None:
-        segments = ((0, rows, w.gs),)
-    n = len(segments)
-    if n > MAX_SEGMENTS:
-        raise ValueError("too many segments")
-    segs = (Segment * n)(*[Segment(n0, n1, _ptr(g)) for n0, n1, g in segments])
-    _launch("nvfp4_matvec", lib().nvfp4_matvec, dev, stream, made, x.data_ptr(), ld_x, x.shape[0],
+        n, segs = 1, Segment(0, rows, w.gs.data_ptr())
+    else:
+        n = len(segments)
+        if n > MAX_SEGMENTS:
+            raise ValueError("too many segments")
+        segs = (Segment * n)(*[Segment(n0, n1, _ptr(g)) for n0, n1, g in segments])
+    _launch("nvfp4_matvec", lib().nvfp4_matvec, dev, stream, (made,), x.data_ptr(), ld_x, x.shape[0],
             Operand(codes.data_ptr(), scales.data_ptr(), rows, cols), segs, n, out.data_ptr(), kind, ldo)
     return out
 

@@ -1133,12 +1133,15 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   const int i = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
   int ctas = dev->sms * (i == 0 ? attn::Cfg<64>::CTAS : i == 1 ? attn::Cfg<128>::CTAS : attn::Cfg<256>::CTAS);
   if (ctas > kMaxAttnCtas) ctas = kMaxAttnCtas;
+  const int tile = i == 0 ? attn::Cfg<64>::TILE : i == 1 ? attn::Cfg<128>::TILE : attn::Cfg<256>::TILE;
+  a.whole = a.max_kv <= int64_t(attn::kWholeTiles) * tile;
   CUtensorMap k_map, v_map;
   const int box = attn::box_log(log_block, cache->head_dim);
   if (!encode_cache_map(&k_map, cache->k, cache, box) || !encode_cache_map(&v_map, cache->v, cache, box))
     return NVFP4_ERR_CUDA;
   auto launch_decode = [&](auto kernel, auto combine, int smem) {
     if (nvfp4_status_t e = launch_pdl(kernel, dim3(ctas), dim3(attn::kThreads), smem, s, 1, a, k_map, v_map)) return e;
+    if (a.whole) return NVFP4_OK;
     const int threads = i == 0 ? attn::Join<64>::THREADS : i == 1 ? attn::Join<128>::THREADS : attn::Join<256>::THREADS;
     return launch_pdl(combine, dim3(static_cast<unsigned>(w.units), attn::kRows / attn::Join<128>::ROWS), dim3(threads), 0, s, 1, a);
   };
