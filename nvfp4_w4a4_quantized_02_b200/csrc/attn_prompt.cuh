@@ -323,6 +323,13 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
       for (int g = 0; g < R / kGroup; ++g) c.ks[j & 7][lane * (R / kGroup) + g] = s;
     }
     if (lane == 0) c.valid[j & 7] = have;
+    if (wanted(j) && blk < 0) {
+      // no such block: what the stage held before may be NaN codes, whose scores no scale would mask
+      for (int p = 0; p < C::PANELS8; ++p)
+        for (int i = 0; i < R * C::ROWB; i += 16)
+          *reinterpret_cast<uint4 *>(kbuf + ks * C::K_BYTES + (p * C::BN + lane * R) * C::ROWB + i) = make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive_expect_tx(&c.k_full[ks], bytes);
     __syncwarp();

@@ -1086,7 +1086,8 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   int log_block = 0;
   if (!q_bf16 || !out || !workspace) return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status_t st = check_batch(batch, cache, &log_block)) return st;
-  if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || !std::isfinite(softmax_scale)) return NVFP4_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || !std::isfinite(softmax_scale * 1.4426950408889634f))
+    return NVFP4_ERR_INVALID_ARG;
   if (out_kind != NVFP4_OUT_BF16 && out_kind != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
   if (n_heads > 65535 || batch->tokens * (n_heads / cache->n_kv_heads) > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const int64_t width = int64_t(n_heads) * cache->head_dim;

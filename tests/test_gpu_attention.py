@@ -279,3 +279,75 @@ def test_mixed_batch_equals_separate_calls(nv):
         # a unit cut elsewhere sums in another order, and takes its weights from other references:
         # each side is within its FP16 rounding of them
         assert torch.allclose(part, whole[lo:lo + n], rtol=0, atol=2.0 ** -10 * float(whole.abs().max()))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 90])
+def test_whole_leading_tiles_of_bad_blocks(nv, q_len, d):
+    def edit(k, v, ks, vs, table):
+        table[0, :17] = 10 ** 6  # the first 272 tokens: more than two tiles
+    got, _ = run_case(nv, [q_len], [700], 3, 1, d, 16, True, edit=edit)
+    assert got.any()
+    assert nv.device_status() == 7
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [2, 70])
+def test_nothing_but_bad_blocks(nv, q_len, d):
+    def edit(k, v, ks, vs, table):
+        table[:] = -1
+    got, _ = run_case(nv, [q_len], [400], 3, 1, d, 16, True, edit=edit)
+    assert not got.any() and nv.device_status() == 7
+
+
+def test_many_sequences(nv):
+    """More sequences than threads of a CTA, short and long in turn."""
+    rng = np.random.default_rng(11)
+    q_lens = [int(x) for x in rng.integers(0, 4, 900)]
+    q_lens[::97] = [45] * len(q_lens[::97])
+    kv_lens = [q + int(x) for q, x in zip(q_lens, rng.integers(0, 60, 900))]
+    kv_lens[500] = 3000
+    run_case(nv, q_lens, kv_lens, 1, 1, 64, 16, True)
+    assert nv.device_status() == 0
+
+
+def test_first_sequence_starts_behind_the_first_row(nv):
+    import torch
+    for q_lens in ([2, 1], [50, 40]):
+        q, cu, lens, table, cache = _inputs(nv, q_lens, [60, 41], 4, 2, 128, 16)
+        want = nv.attention(q, cu, lens, table, cache)
+        more = torch.cat([torch.full_like(q[:3], 5.0), q])
+        out = torch.full_like(more, 9.0)
+        nv.attention(more, cu + 3, lens, table, cache, out=out)
+        assert torch.equal(out[3:], want) and (out[:3] == 9.0).all()
+
+
+def test_two_streams_at_once(nv):
+    import torch
+    runs = []
+    for i, (q_lens, kv_lens) in enumerate((([1] * 6, [4000, 10, 700, 90, 2000, 64]), ([300, 200], [900, 700]))):
+        args = _inputs(nv, q_lens, kv_lens, 6, 2, 128, 64, seed=i)
+        runs.append((args, nv.attention(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for args, want, stream in runs:
+            with torch.cuda.stream(stream):
+                got.append((nv.attention(*args), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+
+
+def test_changed_lengths_between_replays(nv):
+    """A captured call follows the lengths, tables and queries that are in its buffers when it runs."""
+    import torch
+    q, cu, lens, table, cache = _inputs(nv, [1, 1, 1], [900, 900, 900], 4, 2, 128, 16)
+    out = torch.zeros_like(q)
+    nv.attention(q, cu, lens, table, cache, out=out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nv.attention(q, cu, lens, table, cache, out=out)
+    for n in ([1, 2, 3], [900, 1, 450], [16, 17, 0]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        g.replay()
+        assert torch.equal(out, nv.attention(q, cu, lens, table, cache)), n

@@ -178,3 +178,22 @@ def test_graph_and_side_stream(nv):
         ref.append(x, q_lens, kv_lens, table, host[i], host[2 + i], block)
     _check(nv, cache, host)
     _check(nv, again, host)
+
+
+def test_many_sequences(nv):
+    import torch
+    rng = np.random.default_rng(5)
+    q_lens = [int(x) for x in rng.integers(0, 3, 700)]
+    q_lens[13] = 200
+    kv_lens = [q + int(x) for q, x in zip(q_lens, rng.integers(0, 40, 700))]
+    cu, lens, table_d, table, count = batch(q_lens, kv_lens, 16, rng)
+    host = filled_cache(count, 1, 16, 64, rng, 3.0)
+    cache = to_cache(nv, *host)
+    (k, k_d), (v, v_d) = (_rows(sum(q_lens), 1, 64, rng) for _ in range(2))
+    # the first sequence starts behind the first row
+    pad = lambda t: torch.cat([torch.full((4, 64), 7.0, dtype=t.dtype, device="cuda"), t.reshape(len(t), -1)])
+    nv.kv_append(pad(k_d), pad(v_d), cu + 4, lens, table_d, cache)
+    ref.append(k, q_lens, kv_lens, table, host[0], host[2], 16)
+    ref.append(v, q_lens, kv_lens, table, host[1], host[3], 16)
+    _check(nv, cache, host)
+    assert nv.device_status() == 0
