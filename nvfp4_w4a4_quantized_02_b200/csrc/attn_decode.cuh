@@ -80,6 +80,9 @@ struct Args {
   float *part;                // [2 * gridDim.x][kRows][D]
   float2 *part_ml;            // [2 * gridDim.x][kRows] (M, l)
   int whole;                  // units are not cut: no partial results, no combine kernel
+  int splits;                 // prompt kernel: CTAs per item at most (prompt_part, prompt_ml: 1 + splits > 1)
+  float *prompt_part;         // [items * splits][rows of an item][D]
+  float2 *prompt_ml;          // [items * splits][rows of an item] (reference, l)
   int max_decode_rows;        // sequences with more query rows per kv head belong to the prompt kernel
 };
 

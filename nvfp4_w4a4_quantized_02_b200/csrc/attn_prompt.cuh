@@ -228,17 +228,21 @@ struct Item {
   int seq, h, row0;  // first query row of its tiles
   int kv_end;        // cached tokens that some row sees
   int lim_min;       // tokens that every row sees
+  int parts;         // CTAs that share the item's K / V tiles
+  int tok0, tiles;   // first token and number of tiles of this part
 };
 
-// Finds the CTA's work: items of a sequence are (row block, kv head), the row blocks with
-// the most visible tokens first.  Returns false when there is none.
-template <int D>
-__device__ bool find_item(const Args &a, Item &it) {
+// Part `part` of item `index`: items of a sequence are (row block, kv head), the row blocks with
+// the most visible tokens first.  Returns false when there is none.  An item is cut into up to
+// a.splits parts of kMinTiles tiles at least.
+constexpr int kMinTiles = 8;
+template <int D, int THREADS>
+__device__ bool find_item(const Args &a, Item &it, int index, int part) {
   using C = Cfg<D>;
-  __shared__ int64_t s_sum[kThreads / 32], s_before;
+  __shared__ int64_t s_sum[THREADS / 32], s_before;
   __shared__ int s_seq;
   int64_t base = 0;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
+  for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
     const int s = s0 + threadIdx.x;
     int64_t items = 0;
     if (s < a.n_seqs) {
@@ -256,17 +260,17 @@ __device__ bool find_item(const Args &a, Item &it) {
     if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x >> 5] = sum;
     __syncthreads();
     int64_t all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < int(threadIdx.x >> 5)) sum += s_sum[w];
       all += s_sum[w];
     }
-    if (int64_t(blockIdx.x) < base + sum && int64_t(blockIdx.x) >= base + sum - items) {
+    if (index < base + sum && index >= base + sum - items) {
       s_seq = s;
       s_before = base + sum - items;
     }
     __syncthreads();
     if (s_seq >= 0) {
-      const int local = static_cast<int>(blockIdx.x - s_before);
+      const int local = static_cast<int>(index - s_before);
       it.seq = s_seq;
       it.sq = load_seq(a, it.seq);
       const int rows = it.sq.q_len * a.group;
@@ -277,7 +281,12 @@ __device__ bool find_item(const Args &a, Item &it) {
       const int off = it.sq.kv_len - it.sq.q_len + 1;
       it.kv_end = a.causal ? max(0, off + last / a.group) : it.sq.kv_len;
       it.lim_min = a.causal ? max(0, off + it.row0 / a.group) : it.sq.kv_len;
-      return true;
+      const int tiles = (it.kv_end + C::BN - 1) / C::BN;
+      it.parts = min(max(tiles / kMinTiles, 1), a.splits);
+      const int first = static_cast<int>(int64_t(tiles) * part / it.parts);
+      it.tok0 = first * C::BN;
+      it.tiles = static_cast<int>(int64_t(tiles) * (part + 1) / it.parts) - first;
+      return part < it.parts;
     }
     base += all;
     __syncthreads();
@@ -295,7 +304,7 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
   const int log_r = min(a.log_block, C::LOG_BOX), R = 1 << log_r, boxes = C::BN >> log_r;
   const int mask = (1 << a.log_block) - 1;
   const int32_t *row = a.table + it.seq * a.ld_table;
-  auto token = [&](int j) { return j * C::BN + (lane << log_r); };
+  auto token = [&](int j) { return it.tok0 + j * C::BN + (lane << log_r); };
   auto wanted = [&](int j) { return j < n_tiles && lane < boxes && token(j) < it.kv_end; };
   auto lookup = [&](int j) { return wanted(j) ? __ldg(row + (token(j) >> a.log_block)) : -1; };
   auto check = [&](int j, int id) -> int {  // (block, head) index, -1: nothing there
@@ -370,10 +379,10 @@ __device__ void convert(const Args &a, Control<D> &c, const unsigned char *raw, 
     for (int i = 0; i < C::PIECES; ++i)
       x[i] = *reinterpret_cast<const uint4 *>(raw + st * C::K_BYTES + (tid + 128 * i) * 16);
     warp_arrive(&c.raw_empty[st]);
-    if (have != all || (j + 1) * C::BN > it.lim_min) {
+    if (have != all || it.tok0 + (j + 1) * C::BN > it.lim_min) {
 #pragma unroll
       for (int i = 0; i < C::PIECES; ++i) {
-        const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR, tok = j * C::BN + row;
+        const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR, tok = it.tok0 + j * C::BN + row;
         uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         const bool gone = !((have >> (row >> log_r)) & 1) || tok >= it.kv_end;  // bytes that belong to no token
 #pragma unroll
@@ -759,7 +768,7 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const Scales *sc = c.ks[j & 7] + hf * (C::GROUPS / 2);
-    const int col0 = j * C::BN + hf * C::HALF;
+    const int col0 = it.tok0 + j * C::BN + hf * C::HALF;
     const int vis = lim - col0;  // visible columns of this half row
     const bool masked = warp_lim < col0 + C::HALF;
     uint32_t p[C::HALF / 2];
@@ -846,6 +855,8 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
   const int col0 = (C::kSplitKV ? 2 * w + hf : hf) * kCols;
   const int64_t at = (it.sq.start + tok) * a.ld_out + int64_t(head) * D;
   const bool nan_any = *const_cast<volatile int *>(&c.nan_any) != 0;
+  const int64_t part_row = int64_t(blockIdx.x) * C::ROWS + local;  // of the partial results
+  if (it.parts > 1 && col0 == 0) a.prompt_ml[part_row] = make_float2(m_ref, l);
 #pragma unroll 1
   for (int c0 = col0; c0 < col0 + kCols; c0 += 32) {
     uint32_t r[32];
@@ -853,12 +864,12 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
     tmem_ld_wait();
 #pragma unroll
     for (int n = 0; n < 32; ++n) {
-      r[n] = empty ? 0u : __float_as_uint(__uint_as_float(r[n]) * f);
+      if (it.parts == 1) r[n] = empty ? 0u : __float_as_uint(__uint_as_float(r[n]) * f);
       if (nan_any && c.nan_first[c0 + n] < lim) r[n] = 0x7fffffffu;
     }
     if (!valid) continue;
-    if (a.out_fp32) {
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + at + c0);
+    if (it.parts > 1 || a.out_fp32) {
+      uint4 *dst = reinterpret_cast<uint4 *>(it.parts > 1 ? a.prompt_part + part_row * D + c0 : static_cast<float *>(a.out) + at + c0);
 #pragma unroll
       for (int n = 0; n < 8; ++n) dst[n] = make_uint4(r[4 * n], r[4 * n + 1], r[4 * n + 2], r[4 * n + 3]);
     } else {
@@ -877,15 +888,17 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
   }
 }
 
-// Grid: an upper bound of the items; dynamic shared memory smem_bytes<D>().
+// Grid: an upper bound of the items, times a.splits; dynamic shared memory smem_bytes<D>().
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map) {
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_raw[];
   grid_dep_wait();
   grid_dep_launch();
   Item it;
-  if (!find_item<D>(a, it)) return;
+  const int index = blockIdx.x / a.splits;
+  if (!find_item<D, kThreads>(a, it, index, static_cast<int>(blockIdx.x) - index * a.splits)) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (it.kv_end == 0) {  // no row sees a token
     const int n_rows = it.sq.q_len * a.group;
@@ -898,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     return;
   }
-  const int n_tiles = (it.kv_end + C::BN - 1) / C::BN;
+  const int n_tiles = it.tiles;
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned char *qbuf = smem, *kbuf = smem + C::K_OFF, *vbuf = smem + C::V_OFF, *raw = smem + C::RAW_OFF;
   Control<D> &c = *reinterpret_cast<Control<D> *>(smem + C::CTL_OFF);
@@ -960,6 +973,53 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(c.tmem, 512);
+}
+
+// Joins the parts of the items that several CTAs share.  Grid (items, rows of an item / kJoinRows),
+// 16 threads per row.
+constexpr int kJoinRows = 16, kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+  using C = Cfg<D>;
+  grid_dep_wait();
+  grid_dep_launch();
+  Item it;
+  if (!find_item<D, kJoinThreads>(a, it, blockIdx.x, 0) || it.parts == 1) return;
+  const int local = blockIdx.y * kJoinRows + threadIdx.x / 16, R = it.row0 + local;
+  if (R >= it.sq.q_len * a.group) return;
+  const int64_t first = int64_t(blockIdx.x) * a.splits * C::ROWS + local;
+  float M = -INFINITY;
+  for (int p = 0; p < it.parts; ++p) M = fmaxf(M, a.prompt_ml[first + int64_t(p) * C::ROWS].x);
+  const float base = M == -INFINITY ? 0.0f : M;
+  constexpr int N = D / 64;  // float4 per thread
+  float l = 0.0f;
+  float4 o[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) o[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+  for (int p = 0; p < it.parts; ++p) {
+    const int64_t at = first + int64_t(p) * C::ROWS;
+    const float2 ml = a.prompt_ml[at];
+    const float f = ex2(ml.x - base);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float4 v = *reinterpret_cast<const float4 *>(a.prompt_part + at * D + 4 * (threadIdx.x % 16 + 16 * n));
+      o[n].x = fmaf(v.x, f, o[n].x), o[n].y = fmaf(v.y, f, o[n].y), o[n].z = fmaf(v.z, f, o[n].z), o[n].w = fmaf(v.w, f, o[n].w);
+    }
+  }
+  const float f = M == -INFINITY && l == l ? 0.0f : 1.0f / l;  // no visible token, and no NaN score: 0
+  const int64_t row = (it.sq.start + R / a.group) * a.ld_out + int64_t(it.h * a.group + R % a.group) * D;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int64_t at = row + 4 * (threadIdx.x % 16 + 16 * n);
+    if (a.out_fp32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(o[n].x * f, o[n].y * f, o[n].z * f, o[n].w * f);
+    } else {
+      __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o[n].x * f, o[n].y * f), __floats2bfloat162_rn(o[n].z * f, o[n].w * f)};
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = *reinterpret_cast<const uint2 *>(p);
+    }
+  }
 }
 
 }  // namespace prompt

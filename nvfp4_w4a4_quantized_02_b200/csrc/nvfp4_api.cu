@@ -337,9 +337,24 @@ constexpr int kMaxAttnCtas = 640;
 // Sequences with at most this many query rows per kv head (new tokens times heads of a
 // group) go to the decode kernel, the others to the prompt kernel.
 constexpr int kDecodeRows = 32;
+// Few prompt items (row blocks times kv heads) for the SMs: each is cut into as many parts as make
+// the CTAs fill whole waves best (1024 tokens on 32768 at four kv heads of 256 values: 192 items on
+// 148 SMs, 955 us uncut), while the parts' results fit kMaxPromptParts places.
+constexpr int kMaxPromptParts = 640, kMaxSplits = 8, kSmsAssumed = 148;
+int prompt_splits(int64_t items, int most) {
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= most && (s == 1 || items * s <= kMaxPromptParts); ++s) {
+    const double cost = double((items * s + kSmsAssumed - 1) / kSmsAssumed) / s + 0.03 * (s - 1);
+    if (cost < best_cost) best_cost = cost, best = s;
+  }
+  return best;
+}
+
 struct AttnWorkspace {
-  int64_t units;
-  size_t desc, desc2, part_ml, part, bytes;
+  int64_t units, items;  // bounds of the decode units and the prompt items of the call
+  int splits;
+  size_t desc, desc2, part_ml, part, prompt_ml, prompt_part, bytes;
 };
 AttnWorkspace attn_workspace(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim) {
   AttnWorkspace w;
@@ -351,7 +366,15 @@ AttnWorkspace attn_workspace(int64_t tokens, int64_t n_seqs, int n_heads, int n_
   w.desc2 = w.desc + w.units * sizeof(int4);
   w.part_ml = (w.desc2 + w.units * sizeof(int2) + 255) / 256 * 256;
   w.part = w.part_ml + size_t(2) * kMaxAttnCtas * attn::kRows * sizeof(float2);
-  w.bytes = w.part + size_t(2) * kMaxAttnCtas * attn::kRows * head_dim * sizeof(float);
+  w.prompt_ml = w.part + size_t(2) * kMaxAttnCtas * attn::kRows * head_dim * sizeof(float);
+  // a prompt has more than kDecodeRows rows; its last row block may be short
+  const int64_t rows = tokens * group, tile = head_dim == 256 ? 128 : 256;
+  const int64_t prompts = rows / (kDecodeRows + 1) < n_seqs ? rows / (kDecodeRows + 1) : n_seqs;
+  w.items = (rows / tile + prompts) * n_kv_heads;
+  w.splits = prompt_splits(w.items, kMaxSplits);
+  const size_t parts = w.splits > 1 ? size_t(w.items) * w.splits * tile : 0;
+  w.prompt_part = w.prompt_ml + (parts * sizeof(float2) + 255) / 256 * 256;
+  w.bytes = w.prompt_part + parts * head_dim * sizeof(float);
   return w;
 }
 
@@ -1152,20 +1175,27 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
     return e;
   // Only the device knows the sequences' lengths; no prompt fits in few rows.
   const int64_t rows = batch->tokens * a.group;
-  if (rows <= kDecodeRows) return NVFP4_OK;
+  if (rows <= kDecodeRows || w.items == 0) return NVFP4_OK;
   const int most = i == 2 ? attn::prompt::Cfg<256>::LOG_BOX : attn::prompt::Cfg<128>::LOG_BOX;
   if (!encode_cache_map(&k_map, cache->k, cache, log_block < most ? log_block : most)) return NVFP4_ERR_CUDA;
-  auto launch_prompt = [&](auto kernel, int tile_rows, int smem) {
-    const int64_t items = (rows / tile_rows + batch->n_seqs) * a.kv_heads;
-    if (items > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(attn::prompt::kThreads), smem, s, 1, a,
-                      k_map);
+  const int64_t prompt_tiles = a.max_kv / (i == 2 ? attn::prompt::Cfg<256>::BN : attn::prompt::Cfg<128>::BN);
+  const int64_t most_splits = prompt_tiles / attn::prompt::kMinTiles;
+  a.splits = prompt_splits(w.items, most_splits < 1 ? 1 : most_splits < w.splits ? static_cast<int>(most_splits) : w.splits);
+  a.prompt_ml = reinterpret_cast<float2 *>(base + w.prompt_ml);
+  a.prompt_part = reinterpret_cast<float *>(base + w.prompt_part);
+  auto launch_prompt = [&](auto kernel, auto join, int tile_rows, int smem) {
+    if (w.items * a.splits > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (nvfp4_status_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(w.items * a.splits)),
+                                      dim3(attn::prompt::kThreads), smem, s, 1, a, k_map))
+      return e;
+    if (a.splits == 1) return NVFP4_OK;
+    return launch_pdl(join, dim3(static_cast<unsigned>(w.items), tile_rows / attn::prompt::kJoinRows),
+                      dim3(attn::prompt::kJoinThreads), 0, s, 1, a);
   };
-  if (i == 0)
-    return launch_prompt(attn::prompt::prompt_kernel<64>, attn::prompt::Cfg<64>::ROWS, attn::prompt::smem_bytes<64>());
-  if (i == 1)
-    return launch_prompt(attn::prompt::prompt_kernel<128>, attn::prompt::Cfg<128>::ROWS, attn::prompt::smem_bytes<128>());
-  return launch_prompt(attn::prompt::prompt_kernel<256>, attn::prompt::Cfg<256>::ROWS, attn::prompt::smem_bytes<256>());
+  namespace ap = attn::prompt;
+  if (i == 0) return launch_prompt(ap::prompt_kernel<64>, ap::join_kernel<64>, ap::Cfg<64>::ROWS, ap::smem_bytes<64>());
+  if (i == 1) return launch_prompt(ap::prompt_kernel<128>, ap::join_kernel<128>, ap::Cfg<128>::ROWS, ap::smem_bytes<128>());
+  return launch_prompt(ap::prompt_kernel<256>, ap::join_kernel<256>, ap::Cfg<256>::ROWS, ap::smem_bytes<256>());
 }
 
 nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const nvfp4_operand_t *W,

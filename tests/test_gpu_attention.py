@@ -351,3 +351,21 @@ def test_changed_lengths_between_replays(nv):
         lens.copy_(torch.tensor(n, dtype=torch.int32))
         g.replay()
         assert torch.equal(out, nv.attention(q, cu, lens, table, cache)), n
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens", [([40], [4500]), ([60, 1, 45], [3333, 2100, 45]), ([130], [2200])], ids=str)
+def test_few_prompt_rows_on_a_long_cache(nv, d, q_lens, kv_lens):
+    """The cache is cut over several CTAs, whose results are joined."""
+    run_case(nv, q_lens, kv_lens, 2, 1, d, 32, True, seed=8)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_joined_parts_keep_masks_and_nan(nv, d):
+    def edit(k, v, ks, vs, table):
+        v[table[0, 100], 0, 3, 9] = 0x7F       # position 1603: everyone sees it, value 9
+        v[table[0, -1], 0, 5, 17] = 0xFF       # among the new tokens
+        k[table[0, -1], 0, 6, 1] = 0x7F
+        table[0, 20:60] = -3
+    got, _ = run_case(nv, [50], [4090], 2, 1, d, 16, True, edit=edit)
+    assert np.isnan(got[:, :, 9]).all() and not np.isnan(got[0, 0, 8]) and nv.device_status() == 7
