@@ -8,32 +8,30 @@
 //    lo = E4M3(q - hi).  A BF16 value has 8 significant bits and each part holds 4, so the sum is exact
 //    down to 2^-10 of the row's largest value (and to 2^-18 of it in absolute terms below).  Two FP8
 //    products cost what one in FP16 would, and K needs no conversion.
-//  * O += P V runs in FP16, since P needs more than 8 bits of range and precision: a converter
-//    warpgroup turns V codes (exact in FP16) into panels of 64 values with 128-byte swizzle,
-//    token rows, which the product reads as an MN-major operand.
-// S accumulates in TMEM; two softmax warpgroups, one per half of its columns, read it one row per
-// thread and write P over their own half of S as FP16, the A operand of O += P V.  Weights are
-// taken relative to a reference per row, 2^kBoostP at the reference, which stays as it is while the
-// weights fit FP16: a tile costs one pass over S, and the sums of its weights tell whether they did
-// (a sum below FP16's largest value holds none above it).  When one did not (and at the first tile)
-// the warpgroups agree on the rows' maxima, O, which stays in TMEM, is rescaled and the tile's weights
-// are taken again.
+//  * O += P V runs in FP16, since P needs more than 8 bits of range and precision: converter
+//    warps load V codes (exact in FP16) and write panels of 64 values with 128-byte swizzle, token
+//    rows, which the product reads as an MN-major operand.
+// S accumulates in TMEM; a softmax thread reads a row of it and writes P over it as FP16, the A
+// operand of O += P V.  Weights are taken relative to a reference per row, 2^kBoostP at the
+// reference, which stays as it is while the weights fit FP16: a tile costs one pass over S, and the sum
+// of its weights tells whether they did (a sum below FP16's largest value holds none above it).  When
+// they did not (and at the first tile) the row's maximum becomes its reference, O, which stays in
+// TMEM, is rescaled and the tile's weights are taken again.
 //
 // Two streams keep the tensor cores busy while the other's softmax runs.  Up to 128 values per
-// head they are two tiles of query rows with their own O over the same K / V tiles of 128
-// tokens; at 256 values TMEM holds one O and four S of 64 tokens, and the streams are the even and odd
-// K / V tiles, which hand the rows' reference maxima to each other.
+// head they are two tiles of query rows with their own O over the same K / V tiles; at 256 values TMEM
+// holds one O, and the streams are the even and odd K / V tiles, which hand the rows' references to
+// each other.
 //
-// A product of 128 x 128 x 32 bytes takes 64 cycles and a warp needs about 55 to issue one
-// (measured with descriptors ready in registers; a warp that computes them falls to 75).  At 256
-// values S comes in products of 64 columns, which take half as long: there S and O have an issuer each.
+// Bounds.  Per tile of 128 tokens and stream, at 128 (256) values: the tensor cores 1024 (2048) cycles;
+// shared memory, which an SM reads and writes at 128 bytes per cycle, 1024 (2304): the products read
+// 64 (128) KB for S and 32 (64) KB for P V, the converters write 16 (64), the TMA 8 (32); the MUFU 1024
+// (1024) for the exponentials.  A product of 128 x 128 x 32 bytes takes 64 cycles, and a warp needs about
+// 55 to issue one with its descriptors ready (75 if it computes them).
 //
-// Warps (one CTA per SM): 0 and 2 MMA issuers, 1 producer (block table, scales, copies), 3 idle, 4-11
-// and 12-19 softmax of stream 0 and 1 (four warps per half), 20-23 V converter.  Registers are
-// handed from the first and the last warpgroup to the softmax.
-//
-// A wait that runs out sets `ok` to false in the thread that saw it; softmax threads go on through
-// the barriers of their stream without working, so that no one waits for them forever.
+// Warps (one CTA per SM): 0 MMA issuer, 1 producer (block table, scales, K copies), 2-3 idle, 4-7 and
+// 8-11 softmax of stream 0 and 1, 12-19 V converters.  Registers are handed from the others to the
+// softmax.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -42,10 +40,11 @@ namespace nvfp4 {
 namespace attn {
 namespace prompt {
 
-constexpr int kThreads = 768;
-constexpr int kSoftmax = 512;    // softmax threads
-// Registers per thread: 768 threads are launched with 80; 16 * 88 + 4 * 80 + 4 * 48 = 24 * 80.
-constexpr int kRegsSoftmax = 88, kRegsConvert = 80, kRegsOther = 48;
+constexpr int kThreads = 640;
+constexpr int kSoftmax = 256;    // softmax threads
+constexpr int kConverters = 256;
+// Registers per thread: 640 threads are launched with 96; 8 * 144 + 8 * 64 + 4 * 64 = 20 * 96.
+constexpr int kRegsSoftmax = 144, kRegsConvert = 64, kRegsOther = 64;
 constexpr int kTile = 128;      // query rows of a tile
 constexpr float kMostSum = 60000.0f;  // weights whose sum is below this are within FP16
 constexpr float kBoostP = 6.0f;
@@ -54,32 +53,29 @@ template <int D>
 struct Cfg {
   static constexpr bool kSplitKV = D == 256;           // streams are K / V tiles, not row tiles
   static constexpr int NQ = kSplitKV ? 1 : 2;
-  static constexpr int BN = kSplitKV ? 64 : 128;       // cached tokens of a tile
+  static constexpr int BN = 128;                       // cached tokens of a tile
+  static constexpr int VT = kSplitKV ? 64 : 128;       // tokens of a V stage
+  static constexpr int VSUB = BN / VT;
   static constexpr int ROWB = D < 128 ? D : 128;       // bytes of a row of a panel of codes
   static constexpr int PANELS8 = D / ROWB;             // panels of codes
   static constexpr int Q_PART = kTile * D;             // one part of one query tile
   static constexpr int Q_BYTES = NQ * 2 * Q_PART;
   static constexpr int K_BYTES = BN * D;
-  static constexpr int V_BYTES = BN * D * 2;
-  static constexpr int K_STAGES = 3;
+  static constexpr int V_BYTES = VT * D * 2;
+  static constexpr int K_STAGES = kSplitKV ? 2 : 3;
   static constexpr int GROUPS = BN / kGroup;
-  static constexpr int LOG_BOX = kSplitKV ? 6 : 7;     // rows of a TMA box at most: a tile
+  static constexpr int LOG_BOX = 7;                    // rows of a TMA box at most: a tile
   static constexpr int CPR = D / 16;                   // 16-byte pieces of a row of codes
-  static constexpr int PIECES = BN * CPR / 128;        // per converter thread
+  static constexpr int PIECES = VT * CPR / kConverters;  // per converter thread and V stage
   static constexpr int ROWS = NQ * kTile;
-  static constexpr int SLOTS = kSplitKV ? 4 : 2;       // S buffers: one per stream, or per tile in flight
-  static constexpr int HALF = BN / 2;                  // columns of a softmax warpgroup
   static constexpr int O_COL0 = 256;
-  // shared memory: Q, K stages, V (FP16) x 2, V codes x 2
-  static constexpr int K_OFF = Q_BYTES, V_OFF = K_OFF + K_STAGES * K_BYTES, RAW_OFF = V_OFF + 2 * V_BYTES,
-                       CTL_OFF = RAW_OFF + 2 * K_BYTES;
+  // shared memory: Q, K stages, V (FP16) x 2
+  static constexpr int K_OFF = Q_BYTES, V_OFF = K_OFF + K_STAGES * K_BYTES, CTL_OFF = V_OFF + 2 * V_BYTES;
 };
 
-// S buffer of stream w's tile j, and the parity of the phase that its barriers go through for it.
+// Parity of the phase that a stream's barriers go through for its tile j.
 template <int D>
-__device__ __forceinline__ int slot(int w, int j) { return Cfg<D>::kSplitKV ? j & 3 : w; }
-template <int D>
-__device__ __forceinline__ uint32_t phase(int j) { return (Cfg<D>::kSplitKV ? j >> 2 : j) & 1; }
+__device__ __forceinline__ uint32_t phase(int j) { return (Cfg<D>::kSplitKV ? j >> 1 : j) & 1; }
 
 struct Scales {
   float k, log_v, inv_v, pad;
@@ -87,20 +83,20 @@ struct Scales {
 
 template <int D>
 struct Control {
-  uint64_t q_ready, k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2],
-      s_ready[4], p_ready[4], o_done[4], m_ready[2], join, done[2];  // s_ready, p_ready, o_done: by S buffer
+  uint64_t q_ready, k_full[3], k_empty[3], ids_full[8], v_full[2], v_empty[2];
+  uint64_t s_ready[2], p_ready[2], o_done[2], m_ready[2];  // by stream
+  uint64_t join, done;
   uint32_t tmem;
   int nan_any;
-  // Scales and the mask of the groups that hold tokens, by tile.  A slot comes up again eight
+  // Scales and (block, head) indexes (-1: no tokens) by tile.  A slot comes up again eight
   // tiles later; a tile's K is loaded at most three tiles ahead of the products with K, and those
   // are issued at most two tiles ahead of the last softmax that is not done.
   Scales ks[8][Cfg<D>::GROUPS];
-  uint32_t valid[8];
+  int blk[8][Cfg<D>::GROUPS];    // by 16-token group
   int nan_first[D];
   float rc[Cfg<D>::ROWS];        // score scale of each query row, times log2(e)
-  float mx[2][2][kTile];         // by stream and half: maximum of a row's half
   float m_ref[2][kTile];         // kSplitKV: reference maxima of the rows, by parity of the tile
-  float l[4][kTile];
+  float l[2][kTile];             // kSplitKV
 };
 
 template <int D>
@@ -201,6 +197,14 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // Generic-proxy writes to shared memory become visible to the tensor cores.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -295,10 +299,10 @@ __device__ bool find_item(const Args &a, Item &it, int index, int part) {
 }
 
 // Producer warp.  A tile consists of BN / R boxes of R consecutive tokens of one cache block; lane i
-// looks up, and copies, box i.
+// looks up box i, publishes where it is and its scales, and copies its K.
 template <int D>
-__device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, unsigned char *kbuf, unsigned char *raw,
-                        const Item &it, int n_tiles) {
+__device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, unsigned char *kbuf, const Item &it,
+                        int n_tiles) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   const int log_r = min(a.log_block, C::LOG_BOX), R = 1 << log_r, boxes = C::BN >> log_r;
@@ -319,19 +323,21 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
   float sk = blk >= 0 ? __ldg(a.k_scales + blk) : 0.0f, sv = blk >= 0 ? __ldg(a.v_scales + blk) : 1.0f;
 #pragma unroll 1
   for (int j = 0; j < n_tiles; ++j) {
-    const int ks = j % C::K_STAGES, rs = j & 1;
-    const uint32_t have = __ballot_sync(0xffffffffu, blk >= 0);
-    const uint32_t bytes = __popc(have) * (R * D);
-    if (!mbar_wait(&c.k_empty[ks], ((j / C::K_STAGES) & 1) ^ 1)) return;
+    const int ks = j % C::K_STAGES;
     if (lane < boxes) {
       Scales s;
       s.k = sk;
       s.log_v = blk >= 0 ? log_scale(sv) : -INFINITY;  // no such block: nothing to see
       s.inv_v = blk >= 0 ? inverse_scale(sv) : 0.0f;
       s.pad = 0.0f;
-      for (int g = 0; g < R / kGroup; ++g) c.ks[j & 7][lane * (R / kGroup) + g] = s;
+      for (int g = 0; g < R / kGroup; ++g) {
+        c.ks[j & 7][lane * (R / kGroup) + g] = s;
+        c.blk[j & 7][lane * (R / kGroup) + g] = blk;
+      }
     }
-    if (lane == 0) c.valid[j & 7] = have;
+    warp_arrive(&c.ids_full[j & 7]);
+    const uint32_t have = __ballot_sync(0xffffffffu, blk >= 0);
+    if (!mbar_wait(&c.k_empty[ks], ((j / C::K_STAGES) & 1) ^ 1)) return;
     if (wanted(j) && blk < 0) {
       // no such block: what the stage held before may be NaN codes, whose scores no scale would mask
       for (int p = 0; p < C::PANELS8; ++p)
@@ -340,20 +346,13 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
       fence_async_smem();
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(&c.k_full[ks], bytes);
+    if (lane == 0) mbar_arrive_expect_tx(&c.k_full[ks], __popc(have) * (R * D));
     __syncwarp();
-    const int tok = token(j);
     if (blk >= 0) {
 #pragma unroll
       for (int p = 0; p < C::PANELS8; ++p)
-        tma_load_3d(kbuf + ks * C::K_BYTES + (p * C::BN + lane * R) * C::ROWB, k_map, &c.k_full[ks], p * 128, tok & mask, blk);
+        tma_load_3d(kbuf + ks * C::K_BYTES + (p * C::BN + lane * R) * C::ROWB, k_map, &c.k_full[ks], p * 128, token(j) & mask, blk);
     }
-    if (!mbar_wait(&c.raw_empty[rs], ((j >> 1) & 1) ^ 1)) return;
-    if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[rs], bytes);
-    __syncwarp();
-    if (blk >= 0)
-      bulk_load(raw + rs * C::K_BYTES + lane * R * D, a.v + ((int64_t(blk) << a.log_block) + (tok & mask)) * D, R * D,
-                &c.raw_full[rs]);
     blk = check(j + 1, next_id);
     sk = blk >= 0 ? __ldg(a.k_scales + blk) : 0.0f;
     sv = blk >= 0 ? __ldg(a.v_scales + blk) : 1.0f;
@@ -361,66 +360,96 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
   }
 }
 
-// Converter warpgroup (tid 0..127): tile after tile of V codes into FP16.
+// Converter threads: V stage after V stage of codes into FP16, the next stage's codes on their way to
+// registers meanwhile.  Four warps with the same registers in all are slower (8192-token prompt 889 us
+// against 807), as are two stages on their way, whose registers spill (871).
 template <int D>
-__device__ void convert(const Args &a, Control<D> &c, const unsigned char *raw, unsigned char *vbuf, const Item &it,
-                        int n_tiles, int tid) {
+struct Converter {
   using C = Cfg<D>;
-  const int log_r = min(a.log_block, C::LOG_BOX);
-  const uint32_t all = C::BN >> log_r == 32 ? 0xffffffffu : (1u << (C::BN >> log_r)) - 1;
+  const Args &a;
+  Control<D> &c;
+  const Item &it;
+  int n, tid;  // stages in all
+
+  // Piece k of a stage: 16 bytes of row tid / CPR + k STEP
+  static constexpr int STEP = kConverters / C::CPR;
+  static_assert(STEP % 8 == 0 && C::VT % STEP == 0, "the swizzle repeats every 8 rows");
+
+  __device__ __forceinline__ bool load(int i, uint4 (&x)[C::PIECES]) const {
+    if (i >= n) return true;
+    const int j = i / C::VSUB;
+    const bool ok = mbar_wait(&c.ids_full[j & 7], (j >> 3) & 1);
+    const int row0 = (i % C::VSUB) * C::VT + tid / C::CPR, tok0 = it.tok0 + j * C::BN + row0;
+    const int *blks = c.blk[j & 7];
+    const unsigned char *v = reinterpret_cast<const unsigned char *>(a.v) + 16 * (tid % C::CPR);
+#pragma unroll
+    for (int k = 0; k < C::PIECES; ++k) {
+      const int64_t blk = ok ? blks[(row0 + k * STEP) / kGroup] : -1;
+      const int tok = tok0 + k * STEP;
+      x[k] = make_uint4(0, 0, 0, 0);  // bytes that belong to no token never reach the product
+      if (blk >= 0 && tok < it.kv_end) x[k] = ld_stream(v + ((blk << a.log_block) + (tok & ((1 << a.log_block) - 1))) * D);
+    }
+    return ok;
+  }
+  __device__ __forceinline__ bool store(int i, unsigned char *vbuf, uint4 (&x)[C::PIECES]) const {
+    const int st = i & 1, row0 = tid / C::CPR, col = tid % C::CPR;
+    if (!mbar_wait(&c.v_empty[st], ((i >> 1) & 1) ^ 1)) return false;
+    if (it.tok0 + (i + 1) * C::VT > it.lim_min) {
 #pragma unroll 1
-  for (int j = 0; j < n_tiles; ++j) {
-    const int st = j & 1;
-    const uint32_t phase = (j >> 1) & 1;
-    if (!mbar_wait(&c.raw_full[st], phase)) return;
-    const uint32_t have = c.valid[j & 7];
-    uint4 x[C::PIECES];
+      for (int m = 0; m < 4 * C::PIECES; ++m) {  // a NaN that some rows must not see: see decode_segment
+        uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < C::PIECES; ++i)
-      x[i] = *reinterpret_cast<const uint4 *>(raw + st * C::K_BYTES + (tid + 128 * i) * 16);
-    warp_arrive(&c.raw_empty[st]);
-    if (have != all || it.tok0 + (j + 1) * C::BN > it.lim_min) {
-#pragma unroll
-      for (int i = 0; i < C::PIECES; ++i) {
-        const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR, tok = it.tok0 + j * C::BN + row;
-        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        const bool gone = !((have >> (row >> log_r)) & 1) || tok >= it.kv_end;  // bytes that belong to no token
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (gone) w[k] = 0;
-          // a NaN that some rows must not see: see decode_segment
-          if (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u)
-            for (int b = 0; b < 4; ++b)
-              if (((w[k] >> (8 * b)) & 0x7f) == 0x7f) {
-                atomicMin(&c.nan_first[16 * col + 4 * k + b], tok);
-                c.nan_any = 1;
-                w[k] &= ~(0xffu << (8 * b));
-              }
+        for (int k = 0; k < C::PIECES; ++k) {
+          if (m == 4 * k) w = x[k].x;
+          if (m == 4 * k + 1) w = x[k].y;
+          if (m == 4 * k + 2) w = x[k].z;
+          if (m == 4 * k + 3) w = x[k].w;
         }
-        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        if ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) == 0) continue;
+        for (int b = 0; b < 4; ++b)
+          if (((w >> (8 * b)) & 0x7f) == 0x7f) {
+            atomicMin(&c.nan_first[16 * col + 4 * (m & 3) + b], it.tok0 + i * C::VT + row0 + (m >> 2) * STEP);
+            c.nan_any = 1;
+            w &= ~(0xffu << (8 * b));
+          }
+#pragma unroll
+        for (int k = 0; k < C::PIECES; ++k) {
+          if (m == 4 * k) x[k].x = w;
+          if (m == 4 * k + 1) x[k].y = w;
+          if (m == 4 * k + 2) x[k].z = w;
+          if (m == 4 * k + 3) x[k].w = w;
+        }
       }
     }
-    if (!mbar_wait(&c.v_empty[st], phase ^ 1)) return;
-    unsigned char *dst = vbuf + st * C::V_BYTES;
+    // every other panel stores its odd piece first: eight lanes then hit distinct banks
+    const int odd = (col >> 2) & 1;
+    unsigned char *dst0 = vbuf + st * C::V_BYTES + panel_offset(C::VT, col >> 2, row0, 2 * (col & 3) + odd);
+    unsigned char *dst1 = vbuf + st * C::V_BYTES + panel_offset(C::VT, col >> 2, row0, 2 * (col & 3) + (odd ^ 1));
 #pragma unroll
-    for (int i = 0; i < C::PIECES; ++i) {
-      const int p = tid + 128 * i, row = p / C::CPR, col = p % C::CPR;
-      // every other panel stores its odd piece first: eight lanes then hit distinct banks
-      const int o = (col >> 2) & 1;
-      const uint2 first = o ? make_uint2(x[i].z, x[i].w) : make_uint2(x[i].x, x[i].y);
-      const uint2 second = o ? make_uint2(x[i].x, x[i].y) : make_uint2(x[i].z, x[i].w);
-      auto half = [](uint2 w) {
-        return make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+    for (int k = 0; k < C::PIECES; ++k) {
+      auto half = [](uint32_t lo, uint32_t hi) {
+        uint4 h;
+        e4m3x4_to_f16x4(lo, h.x, h.y);
+        e4m3x4_to_f16x4(hi, h.z, h.w);
+        return h;
       };
-      *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + o)) = half(first);
-      *reinterpret_cast<uint4 *>(dst + panel_offset(C::BN, col >> 2, row, 2 * (col & 3) + (o ^ 1))) = half(second);
+      *reinterpret_cast<uint4 *>(dst0 + k * STEP * 128) = odd ? half(x[k].z, x[k].w) : half(x[k].x, x[k].y);
+      *reinterpret_cast<uint4 *>(dst1 + k * STEP * 128) = odd ? half(x[k].x, x[k].y) : half(x[k].z, x[k].w);
     }
     fence_async_smem();
-    mbar_arrive(&c.v_full[st]);
+    warp_arrive(&c.v_full[st]);
+    return true;
   }
-}
+  __device__ void run(unsigned char *vbuf) const {
+    uint4 x[C::PIECES];
+    if (!load(0, x)) return;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i)
+      if (!store(i, vbuf, x) || !load(i + 1, x)) return;
+  }
+};
 
-// MMA issuers (whole warps).  All 512 TMEM columns are this CTA's: addresses start at 0.
+// MMA issuer (a whole warp).  All 512 TMEM columns are this CTA's: addresses start at 0.
 // Descriptors are built once; within an operand they differ in the address field.
 template <int D>
 struct Issuer {
@@ -433,13 +462,13 @@ struct Issuer {
   __device__ Issuer(Control<D> &c, uint32_t q, uint32_t k, uint32_t v) : c(c), elected(elect_one()) {
     qd = D < 128 ? sdesc_sw64_kmajor(q) : sdesc_sw128_kmajor(q);
     kd = D < 128 ? sdesc_sw64_kmajor(k) : sdesc_sw128_kmajor(k);
-    vd = sdesc_sw128_mnmajor(v, C::BN * 128);
+    vd = sdesc_sw128_mnmajor(v, C::VT * 128);
   }
 
   // S = (hi + lo) K_j^T of stream w
   __device__ __forceinline__ void qk(int w, int j) const {
     const uint64_t a = qd + (C::kSplitKV ? 0 : w * (2 * C::Q_PART >> 4)), b = kd + (j % C::K_STAGES) * (C::K_BYTES >> 4);
-    const uint32_t s_col = slot<D>(w, j) * C::BN;
+    const uint32_t s_col = w * C::BN;
 #pragma unroll
     for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -448,77 +477,73 @@ struct Issuer {
         for (int s = 0; s < C::ROWB / 32; ++s)
           mma_f8_ss(elected, s_col, a + (part * C::Q_PART + p * kTile * 128 + 32 * s) / 16, b + (p * C::BN * 128 + 32 * s) / 16,
                     kIdescS, (part | p | s) != 0);
-    commit(elected, &c.s_ready[slot<D>(w, j)]);
+    commit(elected, &c.s_ready[w]);
   }
-  // O += P V_j
-  __device__ __forceinline__ void pv(int w, int j) const {
-    const uint64_t b = vd + (j & 1) * (C::V_BYTES >> 4);
-    const uint32_t p_col = slot<D>(w, j) * C::BN, o_col = C::O_COL0 + (C::kSplitKV ? 0 : w * D);
-    constexpr int H = C::HALF / 16;  // k-steps of a half row
+  // O += P V_j, by V stages; `last`: nobody else reads V_j
+  __device__ __forceinline__ bool pv(int w, int j, bool last) const {
+    const uint32_t p_col = w * C::BN, o_col = C::O_COL0 + (C::kSplitKV ? 0 : w * D);
 #pragma unroll
-    for (int s = 0; s < 2 * H; ++s)
-      mma_f16_ts(elected, o_col, p_col + (s / H) * C::HALF + 8 * (s % H), b + s * (2048 / 16), kIdescO, (j | s) != 0);
-    commit(elected, &c.o_done[slot<D>(w, j)]);
+    for (int h = 0; h < C::VSUB; ++h) {
+      const int i = j * C::VSUB + h;
+      bool ok = mbar_wait(&c.v_full[i & 1], (i >> 1) & 1);
+      if (h == 0) ok = ok && mbar_wait(&c.p_ready[w], phase<D>(j));
+      tc_fence_after();
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      const uint64_t b = vd + (i & 1) * (C::V_BYTES >> 4);
+#pragma unroll
+      for (int s = 0; s < C::VT / 16; ++s)
+        mma_f16_ts(elected, o_col, p_col + 8 * (h * (C::VT / 16) + s), b + s * (2048 / 16), kIdescO, (j | h | s) != 0);
+      if (last) commit(elected, &c.v_empty[i & 1]);
+    }
+    commit(elected, &c.o_done[w]);
+    return true;
   }
   __device__ __forceinline__ bool k_full(int j) const {
     const bool ok = mbar_wait(&c.k_full[j % C::K_STAGES], (j / C::K_STAGES) & 1);
     tc_fence_after();
     return __all_sync(0xffffffffu, ok);
   }
-  __device__ __forceinline__ bool p_ready(int w, int j) const {
-    const bool ok = mbar_wait(&c.v_full[j & 1], (j >> 1) & 1) && mbar_wait(&c.p_ready[slot<D>(w, j)], phase<D>(j));
-    tc_fence_after();
-    return __all_sync(0xffffffffu, ok);
-  }
   __device__ __forceinline__ void k_done(int j) const { commit(elected, &c.k_empty[j % C::K_STAGES]); }
-  __device__ __forceinline__ void v_done(int j) const { commit(elected, &c.v_empty[j & 1]); }
 
-  // Issuer w of two.
-  __device__ void run(int w, int n_tiles) const {
+  // The streams in turn: each gets its products in one piece, which keeps the streams half a period
+  // apart (with an issuer each they fell into step, and the tensor cores idled while both took
+  // exponentials: 5040 cycles per tile against 4290).  A stream's next scores go over its P, right
+  // behind the products with it: products of one issuer run in order.
+  __device__ void run(int n_tiles) const {
     if (!__all_sync(0xffffffffu, mbar_wait(&c.q_ready, 0))) return;
     if constexpr (!C::kSplitKV) {
-      // Both streams in turn: each gets its products in one piece, which keeps the streams half a
-      // period apart (with an issuer each they fell into step, and the tensor cores idled while
-      // both took exponentials: 5040 cycles per tile against 4290).
-      if (w == 1) return;
       if (!k_full(0)) return;
       qk(0, 0);
       qk(1, 0);
       k_done(0);
 #pragma unroll 1
       for (int j = 0; j < n_tiles; ++j) {
-        if (!p_ready(0, j)) return;
-        pv(0, j);
+        if (!pv(0, j, false)) return;
         if (j + 1 < n_tiles) {
           if (!k_full(j + 1)) return;
-          qk(0, j + 1);  // over P_j: products of one issuer run in order
+          qk(0, j + 1);
         }
-        if (!p_ready(1, j)) return;
-        pv(1, j);
-        v_done(j);
+        if (!pv(1, j, true)) return;
         if (j + 1 < n_tiles) {
           qk(1, j + 1);
           k_done(j + 1);
         }
       }
-    } else if (w == 0) {  // S, up to four tiles ahead of O
-#pragma unroll 1
-      for (int j = 0; j < n_tiles; ++j) {
+    } else {
+      for (int j = 0; j < 2 && j < n_tiles; ++j) {
         if (!k_full(j)) return;
-        if (j >= 4) {  // the buffer held P_{j-4}
-          const bool ok = mbar_wait(&c.o_done[j & 3], phase<D>(j - 4));
-          tc_fence_after();
-          if (!__all_sync(0xffffffffu, ok)) return;
-        }
-        qk(0, j);
+        qk(j, j);
         k_done(j);
       }
-    } else {  // O
 #pragma unroll 1
       for (int j = 0; j < n_tiles; ++j) {
-        if (!p_ready(0, j)) return;
-        pv(0, j);
-        v_done(j);
+        const int w = j & 1;
+        if (!pv(w, j, true)) return;
+        if (j + 2 < n_tiles) {
+          if (!k_full(j + 2)) return;
+          qk(w, j + 2);
+          k_done(j + 2);
+        }
       }
     }
   }
@@ -582,13 +607,13 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// Maximum of x = s c + e over the thread's half row of S, NaN if there is one; MASK: only the
+// Maximum of x = s c + e over the thread's row of S, NaN if there is one; MASK: only the
 // first `vis` columns.
 template <int D, bool MASK>
 __device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, float rc, int vis) {
   float mt = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < Cfg<D>::HALF / 32; ++i) {
+  for (int i = 0; i < Cfg<D>::BN / 32; ++i) {
     uint32_t v[32];
     tmem_ld_32x32b_x32(s_tmem + 32 * i, v);
     tmem_ld_wait();
@@ -617,18 +642,21 @@ __device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, floa
   return mt;
 }
 
-// P = 2^(x - base) over the half row of S as FP16 in p, sum of P / sV in l; returns the sum of
+// P = 2^(x - base) over the row of S as FP16 in p, sum of P / sV in l; returns the sum of
 // P (NaN if a score is).  MASK: only the first `vis` columns.
 template <int D, bool MASK>
 __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, float rc, float base, int vis,
-                                         uint32_t (&p)[Cfg<D>::HALF / 2], float &l) {
+                                         uint32_t (&p)[Cfg<D>::BN / 2], float &l) {
+  constexpr int N = Cfg<D>::BN / 32;
   float all = 0.0f;
   l = 0.0f;
+  uint32_t buf[2][32];
+  tmem_ld_32x32b_x32(s_tmem, buf[0]);
 #pragma unroll
-  for (int i = 0; i < Cfg<D>::HALF / 32; ++i) {
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(s_tmem + 32 * i, v);
+  for (int i = 0; i < N; ++i) {
+    const uint32_t(&v)[32] = buf[i & 1];
     tmem_ld_wait();
+    if (i + 1 < N) tmem_ld_32x32b_x32(s_tmem + 32 * (i + 1), buf[(i + 1) & 1]);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const Scales s = sc[2 * i + g];
@@ -659,27 +687,6 @@ __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, floa
     }
   }
   return all;
-}
-
-template <int N>
-__device__ __forceinline__ void store_p(uint32_t s_tmem, const uint32_t (&p)[N]) {
-  static_assert(N == 16 || N == 32, "");
-  if constexpr (N == 16) tmem_st_32x32b_x16(s_tmem, p);
-  else tmem_st_32x32b_x32(s_tmem, p);
-}
-
-// Barrier of the 256 softmax threads of stream w; true if `any` was true in one of them.
-__device__ __forceinline__ bool stream_any(int w, bool any) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 256, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(w + 1), "r"(static_cast<uint32_t>(any))
-      : "memory");
-  return r != 0;
 }
 
 // The CTA's query rows in two E4M3 parts, scaled by 2^-e.  A lane holds 16 consecutive values,
@@ -742,9 +749,9 @@ __device__ __forceinline__ void load_queries(const Args &a, Control<D> &c, unsig
   warp_arrive(&c.q_ready);
 }
 
-// Softmax warpgroup of half `hf` of stream w; tid 0..127 is the row of its tile.
+// Softmax warpgroup of stream w; tid 0..127 is the row of its tile.
 template <int D>
-__device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tiles, int w, int hf, int tid) {
+__device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tiles, int w, int tid) {
   using C = Cfg<D>;
   const int n_rows = it.sq.q_len * a.group;
   const int local = (C::kSplitKV ? 0 : w * kTile) + tid, R = it.row0 + local;
@@ -752,58 +759,46 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
   const int tok = valid ? R / a.group : 0, head = it.h * a.group + (valid ? R % a.group : 0);
   const int lim = !valid ? it.kv_end : a.causal ? it.sq.kv_len - it.sq.q_len + tok + 1 : it.sq.kv_len;
   const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
-  bool ok = mbar_wait(&c.q_ready, 0);
+  if (!__all_sync(0xffffffffu, mbar_wait(&c.q_ready, 0))) return;
   const float rc = c.rc[local];
 
   const uint32_t lanes = (tid & ~31) << 16;  // TMEM lane quadrant of the warp
-  const uint32_t o_tmem = lanes + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
+  const uint32_t s_tmem = lanes + w * C::BN, o_tmem = lanes + C::O_COL0 + (C::kSplitKV ? 0 : w * D);
   float m_ref = -INFINITY, l = 0.0f;
-  const int steps = C::kSplitKV ? (n_tiles - w + 1) / 2 : n_tiles;
+  const int step = C::kSplitKV ? 2 : 1;
 #pragma unroll 1
-  for (int i = 0; i < steps; ++i) {
-    const int j = C::kSplitKV ? 2 * i + w : i;
-    const int sl = slot<D>(w, j);
-    const uint32_t s_tmem = lanes + sl * C::BN + hf * C::HALF;
-    ok = ok && mbar_wait(&c.s_ready[sl], phase<D>(j));
-    ok = __all_sync(0xffffffffu, ok);
+  for (int j = C::kSplitKV ? w : 0; j < n_tiles; j += step) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&c.s_ready[w], phase<D>(j)))) return;
     tc_fence_after();
-    const Scales *sc = c.ks[j & 7] + hf * (C::GROUPS / 2);
-    const int col0 = it.tok0 + j * C::BN + hf * C::HALF;
-    const int vis = lim - col0;  // visible columns of this half row
-    const bool masked = warp_lim < col0 + C::HALF;
-    uint32_t p[C::HALF / 2];
+    const Scales *sc = c.ks[j & 7];
+    const int col0 = it.tok0 + j * C::BN, vis = lim - col0;  // visible columns of this row
+    const bool masked = warp_lim < col0 + C::BN;
+    uint32_t p[C::BN / 2];
     float add = 0.0f;
-    // The reference that the other stream's tile j - 1 left (kSplitKV).
+    // Takes up the reference that the other stream's tile j - 1 left (kSplitKV); 0: as it was, 1: moved, -1: failed.
     auto follow = [&] {
-      ok = ok && mbar_wait(&c.m_ready[w ^ 1], w == 1 ? i & 1 : (i - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
+      if (!__all_sync(0xffffffffu, mbar_wait(&c.m_ready[w ^ 1], phase<D>(j - 1)))) return -1;
       const float m = c.m_ref[(j - 1) & 1][tid];
       const bool moved = m != m_ref;
       if (moved) l *= m_ref == -INFINITY ? 0.0f : ex2(m_ref - m);
       m_ref = m;
-      return __any_sync(0xffffffffu, moved);
+      return __any_sync(0xffffffffu, moved) ? 1 : 0;
     };
-    if (C::kSplitKV && j == 1) follow();
-    bool over = j == 0;  // no reference yet: straight to the maxima
+    if (C::kSplitKV && j == 1 && follow() < 0) return;
+    bool over = j == 0;  // no reference yet: straight to the maximum
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       if (pass == 1 || !over) {
-        float all = 0.0f;
-        if (ok) {
-          const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kBoostP;
-          all = masked ? row_exp<D, true>(s_tmem, sc, rc, base, vis, p, add) : row_exp<D, false>(s_tmem, sc, rc, base, vis, p, add);
-        }
+        const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kBoostP;
+        const float all = masked ? row_exp<D, true>(s_tmem, sc, rc, base, vis, p, add) : row_exp<D, false>(s_tmem, sc, rc, base, vis, p, add);
         if (pass == 1) break;
-        over = stream_any(w, !(all < kMostSum) || (m_ref == -INFINITY && all > 0.0f));
+        over = __any_sync(0xffffffffu, !(all < kMostSum) || (m_ref == -INFINITY && all > 0.0f));
       }
-      bool moved = false;
+      int moved = 0;
       if (C::kSplitKV && j > 1) moved = follow();
+      if (moved < 0) return;
       if (over) {
-        float mt = -INFINITY;
-        if (ok) mt = masked ? row_max<D, true>(s_tmem, sc, rc, vis) : row_max<D, false>(s_tmem, sc, rc, vis);
-        c.mx[w][hf][tid] = mt;
-        stream_any(w, false);
-        mt = fmaxf_nan(mt, c.mx[w][hf ^ 1][tid]);
+        const float mt = masked ? row_max<D, true>(s_tmem, sc, rc, vis) : row_max<D, false>(s_tmem, sc, rc, vis);
         if (!(mt < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or infinite score: so is the row
         const bool grow = mt > m_ref;
         const float f = grow ? ex2(m_ref - mt) : 1.0f;
@@ -811,48 +806,46 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
           l *= f;
           m_ref = mt;
         }
-        if (j > 0) {  // O holds the earlier tiles: it may be touched once their products are in
-          ok = ok && mbar_wait(&c.o_done[slot<D>(w, j - 1)], phase<D>(j - 1));
-          ok = __all_sync(0xffffffffu, ok);
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          // O holds the earlier tiles: it may be touched once their products are in
+          if (!__all_sync(0xffffffffu, mbar_wait(&c.o_done[C::kSplitKV ? w ^ 1 : w], phase<D>(j - 1)))) return;
           tc_fence_after();
-          if (ok && __any_sync(0xffffffffu, grow)) scale_o<D / 2>(o_tmem + hf * (D / 2), f);
+          scale_o<D>(o_tmem, f);
         }
       }
       if (!over && !moved) break;
     }
     l += add;
     if constexpr (C::kSplitKV) {
-      if (hf == 0) c.m_ref[j & 1][tid] = m_ref;  // read last for tile j - 1, whose both halves arrived
+      c.m_ref[j & 1][tid] = m_ref;  // last read for tile j - 1, by the thread that let this one go on
       warp_arrive(&c.m_ready[w]);
     }
-    if (ok) {
-      store_p(s_tmem, p);
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(&c.p_ready[sl]);
-    }
+    uint32_t(*half)[32] = reinterpret_cast<uint32_t(*)[32]>(p);
+    tmem_st_32x32b_x32(s_tmem, half[0]);
+    tmem_st_32x32b_x32(s_tmem + 32, half[1]);
+    tmem_st_wait();
+    tc_fence_before();
+    warp_arrive(&c.p_ready[w]);
   }
 
-  // Join the partial sums, then O / l.
-  if constexpr (C::kSplitKV) {
+  if constexpr (C::kSplitKV) {  // join the streams' sums
     warp_arrive(&c.join);
-    ok = ok && mbar_wait(&c.join, 0);
+    if (!__all_sync(0xffffffffu, mbar_wait(&c.join, 0))) return;
     const float m = c.m_ref[(n_tiles - 1) & 1][tid];  // the last reference; l is relative to the one seen last
     if (m != m_ref && m_ref != -INFINITY) l *= ex2(m_ref - m);
     m_ref = m;
+    c.l[w][tid] = l;
+    warp_arrive(&c.join);
+    if (!__all_sync(0xffffffffu, mbar_wait(&c.join, 1))) return;
+    l = c.l[0][tid] + c.l[1][tid];
   }
-  c.l[2 * w + hf][tid] = l;
-  warp_arrive(&c.join);
-  ok = ok && mbar_wait(&c.join, C::kSplitKV ? 1 : 0);
-  l = c.l[2 * w][tid] + c.l[2 * w + 1][tid];
-  if constexpr (C::kSplitKV) l += c.l[2 * (w ^ 1)][tid] + c.l[2 * (w ^ 1) + 1][tid];
-  ok = ok && mbar_wait(&c.o_done[slot<D>(w, n_tiles - 1)], phase<D>(n_tiles - 1));  // the last products, and all before
-  if (!__all_sync(0xffffffffu, ok)) return;
+  // the last products, and all before
+  if (!__all_sync(0xffffffffu, mbar_wait(&c.o_done[C::kSplitKV ? (n_tiles - 1) & 1 : w], phase<D>(n_tiles - 1)))) return;
   tc_fence_after();
   const bool empty = m_ref == -INFINITY && l == l;  // no visible token (a NaN score leaves m_ref, not l)
   const float f = 1.0f / l;
-  constexpr int kCols = C::kSplitKV ? D / 4 : D / 2;
-  const int col0 = (C::kSplitKV ? 2 * w + hf : hf) * kCols;
+  constexpr int kCols = C::kSplitKV ? D / 2 : D;
+  const int col0 = C::kSplitKV ? w * kCols : 0;
   const int64_t at = (it.sq.start + tok) * a.ld_out + int64_t(head) * D;
   const bool nan_any = *const_cast<volatile int *>(&c.nan_any) != 0;
   const int64_t part_row = int64_t(blockIdx.x) * C::ROWS + local;  // of the partial results
@@ -913,29 +906,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n_tiles = it.tiles;
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  unsigned char *qbuf = smem, *kbuf = smem + C::K_OFF, *vbuf = smem + C::V_OFF, *raw = smem + C::RAW_OFF;
+  unsigned char *qbuf = smem, *kbuf = smem + C::K_OFF, *vbuf = smem + C::V_OFF;
   Control<D> &c = *reinterpret_cast<Control<D> *>(smem + C::CTL_OFF);
   if (tid == 0) {
     mbar_init(&c.q_ready, kSoftmax / 32);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.raw_full[i], 1);
-      mbar_init(&c.raw_empty[i], 4);
-      mbar_init(&c.v_full[i], 128);
-      mbar_init(&c.v_empty[i], 1);
-      mbar_init(&c.m_ready[i], 8);
-    }
+    for (int i = 0; i < 8; ++i) mbar_init(&c.ids_full[i], 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&c.k_full[i], 1);
       mbar_init(&c.k_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.v_full[i], kConverters / 32);
+      mbar_init(&c.v_empty[i], 1);
       mbar_init(&c.s_ready[i], 1);
-      mbar_init(&c.p_ready[i], 8);
+      mbar_init(&c.p_ready[i], 4);
       mbar_init(&c.o_done[i], 1);
+      mbar_init(&c.m_ready[i], 4);
     }
     mbar_init(&c.join, kSoftmax / 32);
-    mbar_init(&c.done[0], 1);
-    mbar_init(&c.done[1], 1);
+    mbar_init(&c.done, 1);
     fence_barrier_init();
     c.nan_any = 0;
   }
@@ -948,24 +937,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
 
-  if (warp >= 20) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-    convert<D>(a, c, raw, vbuf, it, n_tiles, tid & 127);
-  } else if (warp >= 4) {
+  if (warp >= 4 && warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     load_queries<D>(a, c, qbuf, it, warp - 4);
-    softmax<D>(a, c, it, n_tiles, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, tid & 127);
+    softmax<D>(a, c, it, n_tiles, (warp - 4) >> 2, tid & 127);
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    Converter<D>{a, c, it, n_tiles * C::VSUB, tid - 12 * 32}.run(vbuf);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 1) {
-      produce<D>(a, &k_map, c, kbuf, raw, it, n_tiles);
-    } else if (warp != 3) {
+      produce<D>(a, &k_map, c, kbuf, it, n_tiles);
+    } else if (warp == 0) {
       Issuer<D> mma(c, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf));
-      mma.run(warp >> 1, __reduce_max_sync(0xffffffffu, n_tiles));  // uniform for the compiler too
-      if (C::kSplitKV || warp == 0) {  // whatever was issued has to end before TMEM is given back
-        commit(mma.elected, &c.done[warp >> 1]);
-        mbar_wait(&c.done[warp >> 1], 0);
-      }
+      mma.run(__reduce_max_sync(0xffffffffu, n_tiles));  // uniform for the compiler too
+      commit(mma.elected, &c.done);  // whatever was issued has to end before TMEM is given back
+      mbar_wait(&c.done, 0);
     }
   }
   __syncwarp();

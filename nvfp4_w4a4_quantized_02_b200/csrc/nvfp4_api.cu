@@ -1178,7 +1178,7 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   if (rows <= kDecodeRows || w.items == 0) return NVFP4_OK;
   const int most = i == 2 ? attn::prompt::Cfg<256>::LOG_BOX : attn::prompt::Cfg<128>::LOG_BOX;
   if (!encode_cache_map(&k_map, cache->k, cache, log_block < most ? log_block : most)) return NVFP4_ERR_CUDA;
-  const int64_t prompt_tiles = a.max_kv / (i == 2 ? attn::prompt::Cfg<256>::BN : attn::prompt::Cfg<128>::BN);
+  const int64_t prompt_tiles = a.max_kv / attn::prompt::Cfg<128>::BN;
   const int64_t most_splits = prompt_tiles / attn::prompt::kMinTiles;
   a.splits = prompt_splits(w.items, most_splits < 1 ? 1 : most_splits < w.splits ? static_cast<int>(most_splits) : w.splits);
   a.prompt_ml = reinterpret_cast<float2 *>(base + w.prompt_ml);
