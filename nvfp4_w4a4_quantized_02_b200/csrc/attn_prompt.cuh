@@ -29,6 +29,12 @@
 // (1024) for the exponentials.  A product of 128 x 128 x 32 bytes takes 64 cycles, and a warp needs about
 // 55 to issue one with its descriptors ready (75 if it computes them).
 //
+// Measured (TFLOP/s at 4 D per visible pair).  8192 tokens, 48 + 8 heads of 128: 800 us, 1030 TFLOP/s, about
+// 3600 cycles for a tile of both streams against the tensor cores' 2048; what is left is a stream's chain
+// S -> exponentials -> P V, which one other stream does not cover.  1024 tokens on 32768, 24 + 4
+// heads of 256: 836 to 864 us, 940 to 970 TFLOP/s; there the products with K leave the converters little of
+// shared memory (with time stamps in the kernel the MMA warp waits for V half of the time).
+//
 // Warps (one CTA per SM): 0 MMA issuer, 1 producer (block table, scales, K copies), 2-3 idle, 4-7 and
 // 8-11 softmax of stream 0 and 1, 12-19 V converters.  Registers are handed from the others to the
 // softmax.
@@ -671,8 +677,8 @@ __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, floa
           if (32 * i + 16 * g + n + 1 >= vis) x.y = -INFINITY;
         }
         // The MUFU's 16 exponentials per clock are one of the bounds where the streams are row
-        // tiles: there one pair in eight goes to the FMA pipe (8192-token prompt 834 -> 804 us; one in
-        // four 820, three in eight 850; at 256 values it only costs issue slots).
+        // tiles: there one pair in eight goes to the FMA pipe (8192-token prompt 824 -> 806 us; one in
+        // four 811, three in eight 825).  At 256 values it only costs issue slots (844 -> 850 us).
         if (!Cfg<D>::kSplitKV && n == 6) {
           x = exp2_poly(x);
         } else {

