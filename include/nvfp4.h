@@ -427,7 +427,7 @@ typedef struct {
   const int32_t *block_table;   /* device int32 [n_seqs x ld_table]; entries of places behind a
                                  * sequence's end are not read */
   int64_t n_seqs, tokens;       /* n_seqs <= 65535; tokens: rows of the q / k / v / out buffers, 0 allowed */
-  int64_t max_blocks, ld_table; /* columns, row stride */
+  int64_t max_blocks, ld_table; /* columns, row stride; max_blocks * block_size < 2^31 - 512 */
 } nvfp4_batch_t;
 
 /*
@@ -500,6 +500,7 @@ NVFP4_API size_t nvfp4_attention_workspace_bytes(int64_t tokens, int64_t n_seqs,
  *   nvfp4_kv_append writes) are exact, others are taken to within 2^-17.
  *   workspace: device, >= nvfp4_attention_workspace_bytes(...) bytes, 16-byte aligned;
  *   contents on entry do not matter.  Calls that share one must not overlap on the GPU.
+ *   out overlaps neither q nor the cache nor the workspace.
  *   Results do not depend on the order in which CTAs run.
  */
 NVFP4_API nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, const nvfp4_batch_t *batch,
@@ -515,7 +516,7 @@ NVFP4_API nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n
  *   per 1024 columns and keeps its BF16 bits down to 2^-29 of their largest; FP32 sums.
  *   x: device BF16 [M x ld_x], 16-byte aligned, ld_x % 8 == 0.  W: as in nvfp4_linear, with
  *   K % 64 == 0 and any number of rows.  segs: as in nvfp4_linear, with
- *   no alignment of their bounds.  out: BF16 or FP32 per out_kind, ldo >= N, any ldo.
+ *   no alignment of their bounds.  out: BF16 or FP32 per out_kind, ldo >= N, any ldo; it does not overlap x.
  */
 NVFP4_API nvfp4_status_t nvfp4_matvec(const void *x_bf16, int64_t ld_x, int64_t M, const nvfp4_operand_t *W,
                                       const nvfp4_segment_t *segs, int nseg, void *out, int out_kind, int64_t ldo,

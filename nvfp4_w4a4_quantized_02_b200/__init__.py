@@ -687,6 +687,8 @@ def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softm
     out, kind, ld_out, made = _out_buffer(q, q.shape, out, out_dtype)
     if tokens == 0 or b.n_seqs == 0:
         return out
+    if made is None and out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q")
     L, made_ws = lib(), None
     if workspace is None:
         need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, width // d, c.n_kv_heads, d)
@@ -712,6 +714,10 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError("the weight is on another device")
     out, kind, ldo, made = _out_buffer(x, (x.shape[0], rows), out, out_dtype)
+    if made is None and out.data_ptr() == x.data_ptr():
+        raise ValueError("out must not be x")
+    if (w.gs if segments is None else x).get_device() != dev or segments and any(g.get_device() != dev for _, _, g in segments):
+        raise ValueError("a global scale is on another device")
     if segments is None:
         n, segs = 1, Segment(0, rows, w.gs.data_ptr())
     else:

@@ -307,8 +307,9 @@ nvfp4_status_t check_batch(const nvfp4_batch_t *b, const nvfp4_block_cache_t *c,
     default: return NVFP4_ERR_UNSUPPORTED_SHAPE;
   }
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  // kernels count cached tokens in 32 bits, up to the end of a tile behind the last
   if (b->n_seqs > 65535 || b->tokens > kMaxDim || c->n_kv_heads > 65535 || c->num_blocks > kMaxDim ||
-      b->max_blocks > (kMaxDim >> *log_block) - 1 || c->num_blocks * c->n_kv_heads > kMaxDim)
+      b->max_blocks > (kMaxDim - 512) >> *log_block || c->num_blocks * c->n_kv_heads > kMaxDim)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(b->cu_seqlens, 4) || !aligned(b->kv_lens, 4) || !aligned(b->block_table, 4) || !aligned(c->k, 16) ||
       !aligned(c->v, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))

@@ -36,6 +36,7 @@ BATCH_REFUSALS = [
     (dict(block=48), dict(), 2), (dict(block=8), dict(), 2), (dict(block=256), dict(), 2),
     (dict(d=96), dict(), 2), (dict(d=512), dict(), 2),
     (dict(), dict(n=70000), 2), (dict(), dict(tokens=1 << 31), 2), (dict(), dict(cols=1 << 30, ld=1 << 30), 2),
+    (dict(), dict(cols=(1 << 25) - 8, ld=1 << 25), 2),  # 2^31 - 512 cached tokens of 64 a block
     (dict(k=P + 8), dict(), 3), (dict(ks=P + 2), dict(), 3), (dict(), dict(cu=P + 2), 3),
 ]
 

@@ -369,3 +369,19 @@ def test_joined_parts_keep_masks_and_nan(nv, d):
         table[0, 20:60] = -3
     got, _ = run_case(nv, [50], [4090], 2, 1, d, 16, True, edit=edit)
     assert np.isnan(got[:, :, 9]).all() and not np.isnan(got[0, 0, 8]) and nv.device_status() == 7
+
+
+def test_output_over_the_input_is_refused(nv):
+    q, cu, lens, table, cache = _inputs(nv, [1, 3], [40, 50], 2, 1, 64, 16)
+    with pytest.raises(ValueError, match="out must not be q"):
+        nv.attention(q, cu, lens, table, cache, out=q)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n_tiles", [1, 2, 3, 4, 7, 9])
+def test_prompts_around_tile_ends(nv, d, n_tiles):
+    """One token less, as many and one more than whole tiles of 128 cached tokens, causal or not."""
+    for extra in (-1, 0, 1):
+        kv = 128 * n_tiles + extra
+        for causal in (True, False):
+            run_case(nv, [65, 70], [kv, max(kv - 57, 70)], 2, 1, d, 16, causal)

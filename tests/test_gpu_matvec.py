@@ -117,3 +117,13 @@ def test_graph_replay(nv):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_refusals_of_the_binding(nv):
+    import torch
+    w = nv.quantize(torch.ones(64, 64, dtype=torch.bfloat16, device="cuda"))
+    x = torch.ones(2, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="out must not be x"):
+        nv.matvec(x, w, out=x)
+    with pytest.raises(ValueError, match="global scale"):
+        nv.matvec(x, w, segments=[(0, 32, w.gs), (32, 64, w.gs.cpu())])
