@@ -51,9 +51,13 @@ constexpr int kSoftmax = 256;    // softmax threads
 constexpr int kConverters = 256;
 // Registers per thread: 640 threads are launched with 96; 8 * 144 + 8 * 64 + 4 * 64 = 20 * 96.
 constexpr int kRegsSoftmax = 144, kRegsConvert = 64, kRegsOther = 64;
+constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+static_assert(kSoftmax * kRegsSoftmax + kConverters * kRegsConvert + 128 * kRegsOther <= kThreads * kRegsLaunch &&
+                  kRegsSoftmax >= kRegsLaunch && kRegsConvert <= kRegsLaunch && kRegsOther <= kRegsLaunch,
+              "setmaxnreg shares out what the block was launched with; dec takes no more than that, inc no less");
 constexpr int kTile = 128;      // query rows of a tile
 constexpr float kMostSum = 60000.0f;  // weights whose sum is below this are within FP16
-constexpr float kBoostP = 6.0f;
+constexpr float kBoostP = 6.0f;  // the sum may be 937 times the reference's weight; smallest normal weight 2^-20 of it
 
 template <int D>
 struct Cfg {
@@ -182,14 +186,6 @@ __device__ __forceinline__ uint64_t sdesc_sw64_kmajor(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
