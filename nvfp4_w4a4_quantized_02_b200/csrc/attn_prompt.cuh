@@ -32,7 +32,7 @@
 // Measured (TFLOP/s at 4 D per visible pair).  8192 tokens, 48 + 8 heads of 128: 800 us, 1030 TFLOP/s, about
 // 3600 cycles for a tile of both streams against the tensor cores' 2048; what is left is a stream's chain
 // S -> exponentials -> P V, which one other stream does not cover.  1024 tokens on 32768, 24 + 4
-// heads of 256: 836 to 864 us, 940 to 970 TFLOP/s; there the products with K leave the converters little of
+// heads of 256: 752 to 819 us, 990 to 1080 TFLOP/s; there the products with K leave the converters little of
 // shared memory (with time stamps in the kernel the MMA warp waits for V half of the time).
 //
 // Warps (one CTA per SM): 0 MMA issuer, 1 producer (block table, scales, K copies), 2-3 idle, 4-7 and
@@ -49,12 +49,7 @@ namespace prompt {
 constexpr int kThreads = 640;
 constexpr int kSoftmax = 256;    // softmax threads
 constexpr int kConverters = 256;
-// Registers per thread: 640 threads are launched with 96; 8 * 144 + 8 * 64 + 4 * 64 = 20 * 96.
-constexpr int kRegsSoftmax = 144, kRegsConvert = 64, kRegsOther = 64;
-constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
-static_assert(kSoftmax * kRegsSoftmax + kConverters * kRegsConvert + 128 * kRegsOther <= kThreads * kRegsLaunch &&
-                  kRegsSoftmax >= kRegsLaunch && kRegsConvert <= kRegsLaunch && kRegsOther <= kRegsLaunch,
-              "setmaxnreg shares out what the block was launched with; dec takes no more than that, inc no less");
+constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;  // registers per thread at launch
 constexpr int kTile = 128;      // query rows of a tile
 constexpr float kMostSum = 60000.0f;  // weights whose sum is below this are within FP16
 constexpr float kBoostP = 6.0f;  // the sum may be 937 times the reference's weight; smallest normal weight 2^-20 of it
@@ -76,9 +71,16 @@ struct Cfg {
   static constexpr int GROUPS = BN / kGroup;
   static constexpr int LOG_BOX = 7;                    // rows of a TMA box at most: a tile
   static constexpr int CPR = D / 16;                   // 16-byte pieces of a row of codes
-  static constexpr int PIECES = VT * CPR / kConverters;  // per converter thread and V stage
+  static constexpr int TURNS = kSplitKV ? 2 : 1;       // groups of converter warps that take V stages in turn
+  static constexpr int PER_V = kConverters / TURNS;    // converter threads of a V stage
+  static constexpr int PIECES = VT * CPR / PER_V;      // 16-byte pieces of each
   static constexpr int ROWS = NQ * kTile;
   static constexpr int O_COL0 = 256;
+  // Registers per thread by role, after setmaxnreg: the softmax takes what the others do not need.
+  static constexpr int REGS_SOFTMAX = kSplitKV ? 136 : 144, REGS_CONVERT = kSplitKV ? 80 : 64, REGS_OTHER = kSplitKV ? 48 : 64;
+  static_assert(kSoftmax * REGS_SOFTMAX + kConverters * REGS_CONVERT + 128 * REGS_OTHER <= kThreads * kRegsLaunch &&
+                    REGS_SOFTMAX >= kRegsLaunch && REGS_CONVERT <= kRegsLaunch && REGS_OTHER <= kRegsLaunch,
+                "setmaxnreg shares out what the block was launched with; dec takes no more than that, inc no less");
   // shared memory: Q, K stages, V (FP16) x 2
   static constexpr int K_OFF = Q_BYTES, V_OFF = K_OFF + K_STAGES * K_BYTES, CTL_OFF = V_OFF + 2 * V_BYTES;
 };
@@ -362,19 +364,21 @@ __device__ void produce(const Args &a, const CUtensorMap *k_map, Control<D> &c, 
   }
 }
 
-// Converter threads: V stage after V stage of codes into FP16, the next stage's codes on their way to
-// registers meanwhile.  Four warps with the same registers in all are slower (8192-token prompt 889 us
-// against 807), as are two stages on their way, whose registers spill (871).
+// Converter threads: V stages of codes into FP16, a thread's next codes on their way to registers
+// meanwhile.  At 256 values per head the products with K leave little of shared memory, a stage takes
+// long, and two groups of four warps take stages in turn: one's loads and fence pass while the other
+// stores (1024 tokens on 32768: 754 us, all eight on one stage 871).  At 128 values all warps take
+// each stage (8192-token prompt 807 us; in turn 858; four warps in all 889).
 template <int D>
 struct Converter {
   using C = Cfg<D>;
   const Args &a;
   Control<D> &c;
   const Item &it;
-  int n, tid;  // stages in all
+  int n, turn, tid;  // stages in all
 
   // Piece k of a stage: 16 bytes of row tid / CPR + k STEP
-  static constexpr int STEP = kConverters / C::CPR;
+  static constexpr int STEP = C::PER_V / C::CPR;
   static_assert(STEP % 8 == 0 && C::VT % STEP == 0, "the swizzle repeats every 8 rows");
 
   __device__ __forceinline__ bool load(int i, uint4 (&x)[C::PIECES]) const {
@@ -444,10 +448,10 @@ struct Converter {
   }
   __device__ void run(unsigned char *vbuf) const {
     uint4 x[C::PIECES];
-    if (!load(0, x)) return;
+    if (!load(turn, x)) return;
 #pragma unroll 1
-    for (int i = 0; i < n; ++i)
-      if (!store(i, vbuf, x) || !load(i + 1, x)) return;
+    for (int i = turn; i < n; i += C::TURNS)
+      if (!store(i, vbuf, x) || !load(i + C::TURNS, x)) return;
   }
 };
 
@@ -649,16 +653,13 @@ __device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, floa
 template <int D, bool MASK>
 __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, float rc, float base, int vis,
                                          uint32_t (&p)[Cfg<D>::BN / 2], float &l) {
-  constexpr int N = Cfg<D>::BN / 32;
   float all = 0.0f;
   l = 0.0f;
-  uint32_t buf[2][32];
-  tmem_ld_32x32b_x32(s_tmem, buf[0]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t(&v)[32] = buf[i & 1];
+  for (int i = 0; i < Cfg<D>::BN / 32; ++i) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(s_tmem + 32 * i, v);
     tmem_ld_wait();
-    if (i + 1 < N) tmem_ld_32x32b_x32(s_tmem + 32 * (i + 1), buf[(i + 1) & 1]);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const Scales s = sc[2 * i + g];
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.k_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.v_full[i], kConverters / 32);
+      mbar_init(&c.v_full[i], C::PER_V / 32);
       mbar_init(&c.v_empty[i], 1);
       mbar_init(&c.s_ready[i], 1);
       mbar_init(&c.p_ready[i], 4);
@@ -940,14 +941,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
 
   if (warp >= 4 && warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     load_queries<D>(a, c, qbuf, it, warp - 4);
     softmax<D>(a, c, it, n_tiles, (warp - 4) >> 2, tid & 127);
   } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-    Converter<D>{a, c, it, n_tiles * C::VSUB, tid - 12 * 32}.run(vbuf);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONVERT));
+    Converter<D>{a, c, it, n_tiles * C::VSUB, C::TURNS == 1 ? 0 : (tid - 12 * 32) / C::PER_V,
+                 C::TURNS == 1 ? tid - 12 * 32 : (tid - 12 * 32) % C::PER_V}.run(vbuf);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == 1) {
       produce<D>(a, &k_map, c, kbuf, it, n_tiles);
     } else if (warp == 0) {
