@@ -417,9 +417,10 @@ typedef struct {
 /* A batch of sequences with new tokens, packed one after another.  Sequence s has the token
  * rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (none is allowed), which are the last of its
  * kv_lens[s] tokens; its position p lives in cache block block_table[s][p / block_size].
- * A sequence whose bounds are not 0 <= start <= end <= tokens, or with kv_lens[s] outside
+ * A sequence whose bounds are not 0 <= start <= end <= tokens, that starts before an earlier
+ * bound within [0, tokens] (cu_seqlens steps back), or with kv_lens[s] outside
  * [0, max_blocks * block_size], is skipped, and a block outside [0, num_blocks) is never
- * touched; both are reported as NVFP4_ERR_DEVICE_INDEX by nvfp4_get_device_status.  Token
+ * touched; all are reported as NVFP4_ERR_DEVICE_INDEX by nvfp4_get_device_status.  Token
  * rows behind the last sequence are left as they are. */
 typedef struct {
   const int32_t *cu_seqlens;    /* device int32 [n_seqs + 1] */

@@ -43,6 +43,7 @@
 
 #include <type_traits>
 
+#include "batch.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -193,21 +194,40 @@ __device__ __forceinline__ int row_exponent(float amax) {
   return e - 15;
 }
 
-// One sequence of the batch.
+// One sequence of the batch; `high`: largest usable bound of the sequences before it.
 struct Seq {
   int64_t start;
   int q_len, kv_len;
   bool ok;
 };
-__device__ __forceinline__ Seq load_seq(const Args &a, int s) {
+__device__ __forceinline__ Seq make_seq(const Args &a, int64_t b, int64_t e, int64_t kv, int64_t high) {
   Seq r;
-  const int64_t b = __ldg(a.cu_seqlens + s), e = __ldg(a.cu_seqlens + s + 1);
-  const int64_t kv = __ldg(a.kv_lens + s);
-  r.ok = b >= 0 && e >= b && e <= a.tokens && kv >= 0 && kv <= a.max_kv;
+  r.ok = bounds_ok(b, e, a.tokens) && b >= high && kv >= 0 && kv <= a.max_kv;
   r.start = r.ok ? b : 0;
   r.q_len = r.ok ? static_cast<int>(e - b) : 0;
   r.kv_len = r.ok ? static_cast<int>(kv) : 0;
   return r;
+}
+// Sequence s by its own bounds.
+__device__ __forceinline__ Seq load_seq(const Args &a, int s) {
+  return make_seq(a, __ldg(a.cu_seqlens + s), __ldg(a.cu_seqlens + s + 1), __ldg(a.kv_lens + s), 0);
+}
+// Whether sequence s starts behind the usable bounds of those before, of which `high` (shared) is the largest; it
+// takes up s's.  All threads call.
+__device__ __forceinline__ bool in_order(const Args &a, int s, int &high) {
+  const int b = __ldg(a.cu_seqlens + s), h = high;
+  __syncthreads();
+  if (threadIdx.x == 0 && b <= a.tokens) high = max(h, b);
+  __syncthreads();
+  return b >= h;
+}
+// Sequence s of this thread (nothing if s is behind the last) as it counts; all threads call, `high` and
+// s_max as in bound_scan.
+template <int THREADS>
+__device__ __forceinline__ Seq scan_seq(const Args &a, int s, int &high, int (&s_max)[THREADS / 32]) {
+  const bool have = s < a.n_seqs;
+  const int64_t b = have ? __ldg(a.cu_seqlens + s) : 0, e = have ? __ldg(a.cu_seqlens + s + 1) : 0;
+  return make_seq(a, b, e, have ? __ldg(a.kv_lens + s) : 0, bound_scan<THREADS>(have, b, a.tokens, high, s_max));
 }
 
 // Shared memory behind the rings; the warps' O are joined in the rings' place.
@@ -220,6 +240,8 @@ struct DecodeSmem {
   int nan_first[D];  // first token, among those that some rows of the unit do not see, whose value is NaN
   int64_t scan_t[kWarps], scan_u[kWarps];
   int64_t base_t, base_u;
+  int scan_b[kWarps], high;
+  int odd;    // some sequence does not count by its own bounds or length
   int found;
 };
 
@@ -606,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(rings + Cfg<D>::RING);
   if (threadIdx.x < kWarps * Cfg<D>::STAGES) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
   fence_barrier_init();
+  if (threadIdx.x == 0) sm.odd = 0;
   __syncthreads();
   uint32_t phases = 0;  // bit i: parity of the next phase of the warp's stage i
   grid_dep_wait();
@@ -614,17 +637,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   // Total work.  Inclusive sums of the last batch of kThreads sequences stay in t_sum, u_sum.
   int64_t total = 0, total_u = 0, t_sum = 0, u_sum = 0;
   int tiles = 0, units = 0;
+  int high = 0;
   auto batch_sums = [&](int s0) {
     tiles = units = 0;
     const int s = s0 + threadIdx.x;
     if (s < a.n_seqs) {
       const Seq q = load_seq(a, s);
-      if (!q.ok && blockIdx.x == 0) record_bad_index();
+      if (!q.ok) sm.odd = 1;
       seq_work<D>(a, q, tiles, units);
     }
     t_sum = int64_t(tiles) * units;
     u_sum = units;
     block_scan(t_sum, u_sum, sm.scan_t, sm.scan_u);
+    if (sm.odd) {  // again, with what the earlier sequences' bounds leave
+      const Seq q = scan_seq<kThreads>(a, s, high, sm.scan_b);
+      if (s < a.n_seqs && !q.ok && blockIdx.x == 0) record_bad_index();
+      seq_work<D>(a, q, tiles, units);
+      t_sum = int64_t(tiles) * units;
+      u_sum = units;
+      block_scan(t_sum, u_sum, sm.scan_t, sm.scan_u);
+    }
   };
   for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
     batch_sums(s0);
@@ -643,8 +675,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   const int64_t begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
 
   // The sequence that holds tile `begin`, and the tiles and units before it.
-  int64_t before_t = 0, before_u = 0;
+  int64_t before_t = 0;
+  int before_u = 0;  // the units fit the combine kernel's grid
   int seq = 0;
+  high = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
     if (threadIdx.x == 0) sm.found = -1;
     if (a.n_seqs > kThreads) batch_sums(s0);
@@ -659,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     if (sm.found >= 0) {
       seq = sm.found;
       before_t = sm.base_t;
-      before_u = sm.base_u;
+      before_u = static_cast<int>(sm.base_u);
       break;
     }
     if (threadIdx.x == kThreads - 1) {
@@ -668,13 +702,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     }
     __syncthreads();
     before_t = sm.base_t;
-    before_u = sm.base_u;
+    before_u = static_cast<int>(sm.base_u);
     __syncthreads();
   }
   __syncthreads();
 
   int64_t at = begin;
   Seq sq = load_seq(a, seq);
+  if (sm.odd) {
+    if (threadIdx.x == 0) sm.high = static_cast<int>(sq.start);
+    __syncthreads();
+  }
   seq_work<D>(a, sq, tiles, units);
   while (at < end) {
     while (at >= before_t + int64_t(tiles) * units) {  // next sequence with work
@@ -682,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       before_u += units;
       if (++seq >= a.n_seqs) return;
       sq = load_seq(a, seq);
+      if (sm.odd && !in_order(a, seq, sm.high)) sq.q_len = 0;
       seq_work<D>(a, sq, tiles, units);
     }
     const int64_t local = at - before_t;

@@ -248,29 +248,37 @@ template <int D, int THREADS>
 __device__ bool find_item(const Args &a, Item &it, int index, int part) {
   using C = Cfg<D>;
   __shared__ int64_t s_sum[THREADS / 32], s_before;
-  __shared__ int s_seq;
+  __shared__ int s_seq, s_bound[THREADS / 32];
   int64_t base = 0;
+  int high = 0;
+  bool odd = false;  // some sequence does not count by its own bounds or length; uniform
+  constexpr int64_t kOdd = int64_t(1) << 48;  // more than THREADS sequences' items: marks one in the sums
   for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
     const int s = s0 + threadIdx.x;
-    int64_t items = 0;
-    if (s < a.n_seqs) {
-      const Seq q = load_seq(a, s);
+    int64_t items, sum, all;
+    for (;;) {
+      Seq q{0, 0, 0, true};
+      if (odd) q = scan_seq<THREADS>(a, s, high, s_bound);
+      else if (s < a.n_seqs) q = load_seq(a, s);
       const int64_t rows = int64_t(q.q_len) * a.group;
-      if (rows > a.max_decode_rows) items = (rows + C::ROWS - 1) / C::ROWS * a.kv_heads;
-    }
-    int64_t sum = items;
+      items = rows > a.max_decode_rows ? (rows + C::ROWS - 1) / C::ROWS * a.kv_heads : 0;
+      sum = odd || q.ok ? items : kOdd;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-      if ((threadIdx.x & 31) >= o) sum += x;
-    }
-    if (threadIdx.x == 0) s_seq = -1;
-    if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < int(threadIdx.x >> 5)) sum += s_sum[w];
-      all += s_sum[w];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        if ((threadIdx.x & 31) >= o) sum += x;
+      }
+      if (threadIdx.x == 0) s_seq = -1;
+      if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x >> 5] = sum;
+      __syncthreads();
+      all = 0;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < int(threadIdx.x >> 5)) sum += s_sum[w];
+        all += s_sum[w];
+      }
+      if (all < kOdd) break;
+      odd = true;  // again, with what the earlier sequences' bounds leave
+      __syncthreads();
     }
     if (index < base + sum && index >= base + sum - items) {
       s_seq = s;

@@ -14,6 +14,7 @@
 // 5.3 TB/s; one new token in each of 32 sequences: 4.4 us, latency.
 #pragma once
 
+#include "batch.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -58,21 +59,39 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   __syncthreads();
   // slots of sequence s: [cu[s] / B + 2 s, cu[s + 1] / B + 2 (s + 1))
   const int64_t slot = blockIdx.x;
-  int64_t first_slot = 0;
+  constexpr int kOdd = 0x7fffffff;  // some sequence does not count by its own bounds
+  auto holds = [&](int s, int64_t c0, int64_t c1) {
+    return (c0 >> a.log_block) + 2 * int64_t(s) <= slot && slot < (c1 >> a.log_block) + 2 * int64_t(s + 1);
+  };
   for (int s = tid; s < a.n_seqs; s += THREADS) {
     const int64_t c0 = __ldg(a.cu_seqlens + s), c1 = __ldg(a.cu_seqlens + s + 1);
-    if (c0 < 0 || c1 < c0 || c1 > a.tokens) {
-      if (slot == 0) record_bad_index();
-    } else if ((c0 >> a.log_block) + 2 * int64_t(s) <= slot && slot < (c1 >> a.log_block) + 2 * int64_t(s + 1)) {
-      s_seq = s;
-    }
+    const bool ok = bounds_ok(c0, c1, a.tokens);
+    if (!ok || holds(s, c0, c1)) atomicMax(&s_seq, ok ? s : kOdd);
   }
   __syncthreads();
+  if (s_seq == kOdd) {  // slot ranges of sequences that do not count may overlap others'
+    __shared__ int s_bound[THREADS / 32];
+    __syncthreads();
+    if (tid == 0) s_seq = -1;
+    int high = 0;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
+      const int s = s0 + tid;
+      const bool have = s < a.n_seqs;
+      const int64_t c0 = have ? __ldg(a.cu_seqlens + s) : 0, c1 = have ? __ldg(a.cu_seqlens + s + 1) : 0;
+      const int before = bound_scan<THREADS>(have, c0, a.tokens, high, s_bound);
+      if (!bounds_ok(c0, c1, a.tokens) || c0 < before) {
+        if (have && slot == 0) record_bad_index();
+      } else if (have && holds(s, c0, c1)) {
+        s_seq = s;
+      }
+    }
+    __syncthreads();
+  }
   const int seq = s_seq;
   if (seq < 0) return;
   const int64_t start = __ldg(a.cu_seqlens + seq), n_new = __ldg(a.cu_seqlens + seq + 1) - start;
   const int64_t total = __ldg(a.kv_lens + seq), past = total - n_new;
-  first_slot = (start >> a.log_block) + 2 * int64_t(seq);
+  const int64_t first_slot = (start >> a.log_block) + 2 * int64_t(seq);
   if (past < 0 || total > a.max_kv) {
     if (tid == 0 && slot == first_slot) record_bad_index();
     return;

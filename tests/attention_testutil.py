@@ -56,3 +56,27 @@ def attention_bound(out, mags, biggest_v, half_step, kv_max):
     2^-14: together below 2^-11 + 2^-13 of sum p |v|.  Weights below 2^-30 of the largest may vanish.
     Then the result is rounded once."""
     return half_step * np.abs(out) + (F16_HALF + 2.0 ** -13) * mags + kv_max * 2.0 ** -30 * biggest_v
+
+
+def counted(cu, tokens):
+    """The sequences of a batch that count: bounds in order and within the rows, and no earlier
+    usable bound behind the start."""
+    out, high = [], 0
+    for s in range(len(cu) - 1):
+        b, e = int(cu[s]), int(cu[s + 1])
+        if 0 <= b <= e <= tokens and b >= high:
+            out.append(s)
+        if b <= tokens:
+            high = max(high, b)
+    return out
+
+
+def broken_bounds(n, longest, rng, share=0.1, first=0):
+    """Bounds of n sequences of up to `longest` new tokens, a share of them (from index `first` on) replaced by
+    anything from -5 to 50 behind the last row."""
+    cu = np.concatenate([[0], np.cumsum(rng.integers(0, longest + 1, n))])
+    tokens = int(cu[-1])
+    wrong = np.flatnonzero(rng.random(n + 1) < share)
+    wrong = wrong[wrong >= first]
+    cu[wrong] = rng.integers(-5, tokens + 50, len(wrong))
+    return cu.astype(np.int32), tokens
