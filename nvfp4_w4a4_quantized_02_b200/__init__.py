@@ -518,17 +518,30 @@ def _rows(x, name: str, dtype, dev: int = -1) -> int:
     return stride[0] if shape[0] > 1 else shape[1]
 
 
-def _launch(what: str, fn, dev: int, stream, made, *args):
+def _made(dev: int, stream, make, returned: bool = True):
+    """``make()``'s buffer for a call on ``stream``, taken from that stream's memory: what the
+    current stream's allocator hands out may still be in use by kernels queued there, and
+    nothing orders ``stream`` behind them.  The caller has a ``returned`` buffer on the
+    current stream, which the allocator has to know of."""
+    if stream is None or stream.cuda_stream == _raw_stream(dev):
+        return make()
+    import torch
+    if stream.device.index != dev:
+        raise ValueError("stream is on another device")
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _launch(what: str, fn, dev: int, stream, *args):
     """Calls an entry point with its device current, on ``stream`` (default: the device's
-    current one).  ``made``: buffers allocated by the caller, which the allocator has to
-    know of when another stream than the current one uses them."""
+    current one)."""
     raw = _raw_stream(dev)
     if stream is not None and stream.cuda_stream != raw:
         if stream.device.index != dev:
             raise ValueError("stream is on another device")
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
         raw = stream.cuda_stream
     if _current_device() == dev:
         status = fn(*args, raw)
@@ -540,8 +553,8 @@ def _launch(what: str, fn, dev: int, stream, made, *args):
         raise NVFP4Error(status, what)
 
 
-def _out_buffer(like, shape, out, out_dtype: str):
-    """(out, kind, row stride, out if it was allocated here) of a BF16 or FP32 result of ``shape``."""
+def _out_buffer(like, shape, out, out_dtype: str, stream):
+    """(out, kind, row stride, whether it was allocated here) of a BF16 or FP32 result of ``shape``."""
     if out_dtype == "bf16":
         dtype, kind = _BF16, 0
     elif out_dtype == "f32":
@@ -549,12 +562,11 @@ def _out_buffer(like, shape, out, out_dtype: str):
     else:
         raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
     if out is None:
-        out = like.new_empty(shape) if kind == 0 else like.new_empty(shape, dtype=dtype)
-        return out, kind, shape[1], out
+        return _made(like.get_device(), stream, lambda: like.new_empty(shape, dtype=dtype)), kind, shape[1], True
     ld = _rows(out, "out", dtype, like.get_device())
     if out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}")
-    return out, kind, ld, None
+    return out, kind, ld, False
 
 
 def _cache_struct(cache: BlockKVCache, dev: int) -> BlockCache:
@@ -590,9 +602,12 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     import torch
     if _BF16 is None:
         _bind_torch()
-    table = torch.empty((max_positions, rot_dim), dtype=torch.float32, device=device)
-    _launch("nvfp4_rope_table", lib().nvfp4_rope_table, table.get_device(), stream, (table,), table.data_ptr(),
-            max_positions, rot_dim, float(base))
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    dev = _current_device() if device.index is None else device.index
+    table = _made(dev, stream, lambda: torch.empty((max_positions, rot_dim), dtype=torch.float32, device=torch.device("cuda", dev)))
+    _launch("nvfp4_rope_table", lib().nvfp4_rope_table, dev, stream, table.data_ptr(), max_positions, rot_dim, float(base))
     return table
 
 
@@ -626,21 +641,20 @@ def qk_norm_rope(q, k, w_q, w_k, positions=None, table=None, *, eps: float = 1e-
             raise ValueError("positions must be a contiguous int64 [tokens] tensor on q's device")
         most, rot = table.shape
         p_pos, p_table = positions.data_ptr(), table.data_ptr()
-    made_q = made_k = None
     if q_out is None:
-        q_out = made_q = q.new_empty((tokens, width_q))
+        q_out = _made(dev, stream, lambda: q.new_empty((tokens, width_q)))
         ld_qo = width_q
     else:
         ld_qo = _rows(q_out, "q_out", bf16, dev)
     if k_out is None:
-        k_out = made_k = q.new_empty((tokens, width_k))
+        k_out = _made(dev, stream, lambda: q.new_empty((tokens, width_k)))
         ld_ko = width_k
     else:
         ld_ko = _rows(k_out, "k_out", bf16, dev)
-    if (made_q is None and q_out.shape != q.shape) or (made_k is None and k_out.shape != k.shape):
+    if q_out.shape != q.shape or k_out.shape != k.shape:
         raise ValueError("q_out / k_out must have the shape of q / k")
     if tokens:
-        _launch("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, dev, stream, (made_q, made_k), q.data_ptr(), ld_q, k.data_ptr(),
+        _launch("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, dev, stream, q.data_ptr(), ld_q, k.data_ptr(),
                 ld_k, tokens, width_q // d, width_k // d, d, w_q.data_ptr(), w_k.data_ptr(), weight_offset, eps,
                 p_pos, p_table, most, rot, interleaved, q_out.data_ptr(), ld_qo, k_out.data_ptr(), ld_ko)
     return q_out, k_out
@@ -660,7 +674,7 @@ def kv_append(k, v, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, strea
         raise ValueError("k and v must be [tokens, n_kv_heads * head_dim] of the cache")
     b = _batch_struct(cu_seqlens, kv_lens, block_table, tokens, dev)
     if tokens and b.n_seqs:
-        _launch("nvfp4_kv_append", lib().nvfp4_kv_append, dev, stream, (), k.data_ptr(), ld_k, v.data_ptr(), ld_v, b, c)
+        _launch("nvfp4_kv_append", lib().nvfp4_kv_append, dev, stream, k.data_ptr(), ld_k, v.data_ptr(), ld_v, b, c)
 
 
 def attention_workspace_bytes(tokens: int, n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -684,18 +698,18 @@ def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softm
     if d == 0 or width % d:
         raise ValueError("q must be [tokens, heads * head_dim] of the cache")
     b = _batch_struct(cu_seqlens, kv_lens, block_table, tokens, dev)
-    out, kind, ld_out, made = _out_buffer(q, q.shape, out, out_dtype)
+    out, kind, ld_out, made = _out_buffer(q, q.shape, out, out_dtype, stream)
     if tokens == 0 or b.n_seqs == 0:
         return out
-    if made is None and out.data_ptr() == q.data_ptr():
+    if not made and out.data_ptr() == q.data_ptr():
         raise ValueError("out must not be q")
-    L, made_ws = lib(), None
+    L = lib()
     if workspace is None:
         need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, width // d, c.n_kv_heads, d)
-        workspace = made_ws = q.new_empty(max(need, 16), dtype=_U8)
+        workspace = _made(dev, stream, lambda: q.new_empty(max(need, 16), dtype=_U8), returned=False)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous, on q's device")
-    _launch("nvfp4_attention", L.nvfp4_attention, dev, stream, (made, made_ws), q.data_ptr(), ld_q, width // d, b, c,
+    _launch("nvfp4_attention", L.nvfp4_attention, dev, stream, q.data_ptr(), ld_q, width // d, b, c,
             d ** -0.5 if softmax_scale is None else softmax_scale, causal, out.data_ptr(), kind, ld_out,
             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
@@ -713,8 +727,8 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
         raise ValueError("x must have the weight's columns")
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError("the weight is on another device")
-    out, kind, ldo, made = _out_buffer(x, (x.shape[0], rows), out, out_dtype)
-    if made is None and out.data_ptr() == x.data_ptr():
+    out, kind, ldo, made = _out_buffer(x, (x.shape[0], rows), out, out_dtype, stream)
+    if not made and out.data_ptr() == x.data_ptr():
         raise ValueError("out must not be x")
     if (w.gs if segments is None else x).get_device() != dev or segments and any(g.get_device() != dev for _, _, g in segments):
         raise ValueError("a global scale is on another device")
@@ -725,7 +739,7 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
         if n > MAX_SEGMENTS:
             raise ValueError("too many segments")
         segs = (Segment * n)(*[Segment(n0, n1, _ptr(g)) for n0, n1, g in segments])
-    _launch("nvfp4_matvec", lib().nvfp4_matvec, dev, stream, (made,), x.data_ptr(), ld_x, x.shape[0],
+    _launch("nvfp4_matvec", lib().nvfp4_matvec, dev, stream, x.data_ptr(), ld_x, x.shape[0],
             Operand(codes.data_ptr(), scales.data_ptr(), rows, cols), segs, n, out.data_ptr(), kind, ldo)
     return out
 
