@@ -192,38 +192,41 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_consta
     load_factors(w);
     from += (g0 * HPW + sub) * D;
     to += (g0 * HPW + sub) * D;
-    const int n = min(g1 * HPW, heads) - (g0 * HPW + sub);  // heads left, from this lane's first on
-    bool odd = false;  // some head's squares were outside FP32's range: it is left to the second pass
+    const int count = g1 - g0, n = min(g1 * HPW, heads) - (g0 * HPW + sub);  // heads left, from this lane's first on
 #pragma unroll 1
-    for (int g = 0; g < g1 - g0; g += kDepth) {
-      const uint16_t *src = from + g * HPW * D;
-      uint16_t *dst = to + g * HPW * D;
-      uint4 raw[kDepth];
+    for (int c0 = 0; c0 < count; c0 += 32) {
+      uint32_t odd = 0;  // bit i: this lane's head of group c0 + i has squares outside FP32's range and is left as it was
+#pragma unroll 1
+      for (int g = c0; g < min(count, c0 + 32); g += kDepth) {
+        const uint16_t *src = from + g * HPW * D;
+        uint16_t *dst = to + g * HPW * D;
+        uint4 raw[kDepth];
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u) {  // `to` may be `from`: no read-only path
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if ((g + u) * HPW < n) raw[u] = *reinterpret_cast<const uint4 *>(src + u * HPW * D);
-      }
+        for (int u = 0; u < kDepth; ++u) {  // `to` may be `from`: no read-only path
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if ((g + u) * HPW < n) raw[u] = *reinterpret_cast<const uint4 *>(src + u * HPW * D);
+        }
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u) {
-        float2 x[4], p[4];
-        expand(raw[u], x, p);
-        const float ss = sum_squares<D>(x);
-        if ((g + u) * HPW < n) {
-          if (outside(ss, a.eps)) odd = true;
-          else store(dst + u * HPW * D, x, p, rsqrt_approx(ss * (1.0f / D) + a.eps));
+        for (int u = 0; u < kDepth; ++u) {
+          float2 x[4], p[4];
+          expand(raw[u], x, p);
+          const float ss = sum_squares<D>(x);
+          if ((g + u) * HPW < n) {
+            if (outside(ss, a.eps)) odd |= 1u << (g - c0 + u);
+            else store(dst + u * HPW * D, x, p, rsqrt_approx(ss * (1.0f / D) + a.eps));
+          }
         }
       }
-    }
-    if (!__any_sync(0xffffffffu, odd)) return;
+      if (!__any_sync(0xffffffffu, odd)) continue;
 #pragma unroll 1
-    for (int g = 0; g < g1 - g0; ++g) {
-      const bool have = g * HPW < n;
-      float2 x[4], p[4];
-      expand(have ? *reinterpret_cast<const uint4 *>(from + g * HPW * D) : make_uint4(0, 0, 0, 0), x, p);
-      const bool again = have && outside(sum_squares<D>(x), a.eps);
-      const float inv = careful_inv_rms<D>(x, p, a.eps);
-      if (again) store(to + g * HPW * D, x, p, inv);
+      for (int i = 0; i < 32; ++i) {
+        const bool again = (odd >> i) & 1;
+        if (!__any_sync(0xffffffffu, again)) continue;
+        float2 x[4], p[4];
+        expand(again ? *reinterpret_cast<const uint4 *>(from + (c0 + i) * HPW * D) : make_uint4(0, 0, 0, 0), x, p);
+        const float inv = careful_inv_rms<D>(x, p, a.eps);
+        if (again) store(to + (c0 + i) * HPW * D, x, p, inv);
+      }
     }
   };
   run(a.q + tok * a.ld_q + first, a.q_out + tok * a.ld_qo + first, a.w_q, a.heads, g_begin, min(g_end, q_groups));

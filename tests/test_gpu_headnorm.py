@@ -126,3 +126,29 @@ def test_no_tokens(nv):
     w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
     a, b = nv.qk_norm_rope(q, q[:, :128], w, w)
     assert a.shape == (0, 256) and b.shape == (0, 128)
+
+
+@pytest.mark.parametrize("tokens", [3, 6000])  # a warp per head group, a warp per token
+@pytest.mark.parametrize("w", [0.0, 2.0 ** -60, 2.0 ** 70])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_in_place_among_heads_outside_fp32(nv, tokens, w, d):
+    """Finished heads whose results are themselves outside FP32's range of squares stay finished."""
+    import torch
+    rng = np.random.default_rng(5)
+    x, x_d, _, _ = _rows(tokens, 9, 5, d, rng)
+    q, k = (t.contiguous().clone() for t in x_d)
+    for t in (q, k):
+        t.reshape(tokens, -1, d)[:, 1::3] *= 2.0 ** 100
+        t.reshape(tokens, -1, d)[:, 2::3] *= 2.0 ** -100
+    weight = torch.full((d,), w, dtype=torch.bfloat16, device="cuda")
+    pos = torch.from_numpy(rng.integers(0, 64, tokens)).cuda()
+    table = nv.rope_table(64, 32)
+    for interleaved in (False, True):
+        want = nv.qk_norm_rope(q, k, weight, weight, pos, table, eps=0.0, interleaved=interleaved)
+        a, b = q.clone(), k.clone()
+        nv.qk_norm_rope(a, b, weight, weight, pos, table, eps=0.0, interleaved=interleaved, q_out=a, k_out=b)
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+        assert bool(want[0].isfinite().all()) and (w > 0 or not want[0].any())
+        some = slice(0, 50)
+        host = q[some].double().cpu().numpy().reshape(-1, 9, d)
+        _check(a[some], ref.head_norm_rope(host, np.full(d, w), 0.0, 0.0, pos[some].cpu().numpy(), table.cpu().numpy(), interleaved), d)
