@@ -11,7 +11,7 @@
 // are read and rewritten only when the scale grows.  The touched blocks are found on
 // the device: sequence s gets the slots from cu[s] / B + 2 s on, at least as many as blocks
 // that cu[s + 1] - cu[s] tokens can touch.  8 sequences of 4096 new tokens, 8 heads of 128 values: 38 us,
-// 5.3 TB/s; one new token in each of 32 sequences: 4.4 us, latency.
+// 5.3 TB/s; one new token in each of 32 sequences: 4.5 us, latency.
 #pragma once
 
 #include "batch.cuh"
@@ -46,47 +46,51 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(max(e, kMinExp) + 127) << 23);
 }
 
+// Whether `slot` is one of sequence s with the bounds c0, c1.
+__device__ __forceinline__ bool holds(int64_t slot, int s, int64_t c0, int64_t c1, int log_block) {
+  return (c0 >> log_block) + 2 * int64_t(s) <= slot && slot < (c1 >> log_block) + 2 * int64_t(s + 1);
+}
+
+// The sequence that has `slot`, where the bounds of some do not count: their slots may overlap others'.
+template <int THREADS>
+__device__ __noinline__ void find_slot(const Args &a, int64_t slot, int &s_seq) {
+  __shared__ int s_bound[THREADS / 32];
+  if (threadIdx.x == 0) s_seq = -1;
+  int high = 0;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
+    const int s = s0 + threadIdx.x;
+    const bool have = s < a.n_seqs;
+    const int64_t c0 = have ? __ldg(a.cu_seqlens + s) : 0, c1 = have ? __ldg(a.cu_seqlens + s + 1) : 0;
+    const int before = bound_scan<THREADS>(have, c0, a.tokens, high, s_bound);
+    if (!bounds_ok(c0, c1, a.tokens) || c0 < before) {
+      if (have && slot == 0) record_bad_index();
+    } else if (have && holds(slot, s, c0, c1, a.log_block)) {
+      s_seq = s;
+    }
+  }
+  __syncthreads();
+}
+
 // Grid (slots, kv_heads, 2: K, V); CHUNKS 16-byte pieces of BF16 rows per thread.
 template <int THREADS, int CHUNKS>
 __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ Args a) {
-  __shared__ int s_seq;
+  __shared__ int s_seq, s_odd;  // s_odd: some sequence does not count by its own bounds
   __shared__ float s_max[THREADS / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x;
   const int B = 1 << a.log_block;
-  if (tid == 0) s_seq = -1;
+  if (tid == 0) s_seq = -1, s_odd = 0;
   __syncthreads();
   // slots of sequence s: [cu[s] / B + 2 s, cu[s + 1] / B + 2 (s + 1))
   const int64_t slot = blockIdx.x;
-  constexpr int kOdd = 0x7fffffff;  // some sequence does not count by its own bounds
-  auto holds = [&](int s, int64_t c0, int64_t c1) {
-    return (c0 >> a.log_block) + 2 * int64_t(s) <= slot && slot < (c1 >> a.log_block) + 2 * int64_t(s + 1);
-  };
   for (int s = tid; s < a.n_seqs; s += THREADS) {
     const int64_t c0 = __ldg(a.cu_seqlens + s), c1 = __ldg(a.cu_seqlens + s + 1);
-    const bool ok = bounds_ok(c0, c1, a.tokens);
-    if (!ok || holds(s, c0, c1)) atomicMax(&s_seq, ok ? s : kOdd);
+    if (!bounds_ok(c0, c1, a.tokens)) s_odd = 1;
+    else if (holds(slot, s, c0, c1, a.log_block)) s_seq = s;
   }
   __syncthreads();
-  if (s_seq == kOdd) {  // slot ranges of sequences that do not count may overlap others'
-    __shared__ int s_bound[THREADS / 32];
-    __syncthreads();
-    if (tid == 0) s_seq = -1;
-    int high = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
-      const int s = s0 + tid;
-      const bool have = s < a.n_seqs;
-      const int64_t c0 = have ? __ldg(a.cu_seqlens + s) : 0, c1 = have ? __ldg(a.cu_seqlens + s + 1) : 0;
-      const int before = bound_scan<THREADS>(have, c0, a.tokens, high, s_bound);
-      if (!bounds_ok(c0, c1, a.tokens) || c0 < before) {
-        if (have && slot == 0) record_bad_index();
-      } else if (have && holds(s, c0, c1)) {
-        s_seq = s;
-      }
-    }
-    __syncthreads();
-  }
+  if (s_odd) find_slot<THREADS>(a, slot, s_seq);
   const int seq = s_seq;
   if (seq < 0) return;
   const int64_t start = __ldg(a.cu_seqlens + seq), n_new = __ldg(a.cu_seqlens + seq + 1) - start;
