@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_consta
     unpack8(raw, x);
     if (a.interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = make_float2(x[i].y, x[i].x);
+      for (int i = 0; i < 4; ++i) p[i] = rotated ? make_float2(x[i].y, x[i].x) : x[i];  // no factor 0 on another value
     } else {
       uint4 o;
       o.x = __shfl_sync(0xffffffffu, raw.x, partner);

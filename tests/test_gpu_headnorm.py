@@ -152,3 +152,26 @@ def test_in_place_among_heads_outside_fp32(nv, tokens, w, d):
         some = slice(0, 50)
         host = q[some].double().cpu().numpy().reshape(-1, 9, d)
         _check(a[some], ref.head_norm_rope(host, np.full(d, w), 0.0, 0.0, pos[some].cpu().numpy(), table.cpu().numpy(), interleaved), d)
+
+
+@pytest.mark.parametrize("rot", [0, 32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_infinities_behind_the_rotation_stay_alone(nv, rot, d):
+    """y = x / rms: next to an infinity finite values are 0, and only rotated pairs share it."""
+    import torch
+    rng = np.random.default_rng(6)
+    x, x_d, w, w_d = _rows(4, 3, 1, d, rng)
+    q = x_d[0].clone()
+    q[1, d + 41] = float("inf")       # behind the rotated range, odd
+    q[2, 2 * d + 50] = -float("inf")  # and even
+    q[3, 7] = float("inf")            # within it, if there is one
+    pos = torch.tensor([3, 5, 7, 9], device="cuda") if rot else None
+    table = nv.rope_table(16, rot) if rot else None
+    out = nv.qk_norm_rope(q, x_d[1], w_d[0], w_d[1], pos, table, interleaved=True)[0].float().reshape(4, 3, d).cpu().numpy()
+    want = np.zeros((4, 3, d), bool)
+    want[1, 1, 41] = want[2, 2, 50] = want[3, 0, 7] = True
+    if rot:
+        want[3, 0, 6] = True
+    assert np.array_equal(np.isnan(out), want)
+    for t, h in ((1, 1), (2, 2), (3, 0)):
+        assert not np.any(out[t, h][~want[t, h]])
