@@ -727,11 +727,17 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
         raise ValueError("x must have the weight's columns")
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError("the weight is on another device")
+    if not (codes.dtype == scales.dtype == _U8 and codes.is_contiguous() and scales.is_contiguous()
+            and codes.numel() >= rows * cols // 2 and scales.numel() >= -(-rows // 128) * 128 * (-(-cols // 64) * 4)):
+        raise ValueError("the weight must be contiguous uint8 codes [rows, cols / 2] and scales of scale_bytes(rows, cols)")
     out, kind, ldo, made = _out_buffer(x, (x.shape[0], rows), out, out_dtype, stream)
     if not made and out.data_ptr() == x.data_ptr():
         raise ValueError("out must not be x")
-    if (w.gs if segments is None else x).get_device() != dev or segments and any(g.get_device() != dev for _, _, g in segments):
-        raise ValueError("a global scale is on another device")
+    for g in (w.gs,) if segments is None else [g for _, _, g in segments]:
+        if g.get_device() != dev:
+            raise ValueError("a global scale is on another device")
+        if g.dtype != _F32 or g.numel() < 1:
+            raise ValueError("a global scale must be a float32 tensor of one value")
     if segments is None:
         n, segs = 1, Segment(0, rows, w.gs.data_ptr())
     else:
