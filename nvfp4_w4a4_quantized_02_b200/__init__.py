@@ -716,7 +716,7 @@ def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softm
 
 
 def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: str = "bf16", out=None, stream=None):
-    """x @ W^T for 1 to 16 token rows x (BF16 [tokens, K], not quantised) and an NVFP4
+    """x @ W^T for up to 16 token rows x (BF16 [tokens, K], not quantised) and an NVFP4
     weight.  segments: list of ``(n_begin, n_end, gs_w)``; default one with ``w.gs``.
     Returns out [tokens, N] (BF16 or FP32)."""
     if _BF16 is None:
@@ -738,6 +738,8 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
             raise ValueError("a global scale is on another device")
         if g.dtype != _F32 or g.numel() < 1:
             raise ValueError("a global scale must be a float32 tensor of one value")
+    if x.shape[0] == 0:
+        return out
     if segments is None:
         n, segs = 1, Segment(0, rows, w.gs.data_ptr())
     else:

@@ -62,3 +62,10 @@ def test_global_scales_of_other_types_are_refused(call):
             call(segments=[(0, 8, _t(torch.ones(1))), (8, 200, _t(gs))])
     with pytest.raises(ValueError, match="another device"):
         call(gs=torch.ones(1))
+
+
+def test_no_tokens_launch_nothing(call):
+    out, launched = call(tokens=0)
+    assert out.shape == (0, 200) and not launched
+    with pytest.raises(ValueError, match="the weight must be"):
+        call(tokens=0, claimed_rows=300)
