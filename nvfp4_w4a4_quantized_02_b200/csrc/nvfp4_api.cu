@@ -356,6 +356,7 @@ struct AttnWorkspace {
   int64_t units, items;  // bounds of the decode units and the prompt items of the call
   int splits;
   size_t desc, desc2, part_ml, part, prompt_ml, prompt_part, bytes;
+  bool fits() const { return units <= kMaxDim && items * splits <= kMaxDim; }  // CTAs of the join and prompt kernels
 };
 AttnWorkspace attn_workspace(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim) {
   AttnWorkspace w;
@@ -1099,7 +1100,8 @@ nvfp4_status_t nvfp4_kv_append(const void *k_bf16, int64_t ld_k, const void *v_b
 size_t nvfp4_attention_workspace_bytes(int64_t tokens, int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim) {
   if (tokens < 0 || n_seqs < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || head_dim < 1) return 0;
   if (tokens > kMaxDim || n_seqs > 65535 || n_heads > 65535 || head_dim > 256) return 0;
-  return attn_workspace(tokens, n_seqs, n_heads, n_kv_heads, head_dim).bytes;
+  const AttnWorkspace w = attn_workspace(tokens, n_seqs, n_heads, n_kv_heads, head_dim);
+  return w.fits() ? w.bytes : 0;
 }
 
 nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, const nvfp4_batch_t *batch,
@@ -1120,6 +1122,7 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
       ld_out % (out_kind == NVFP4_OUT_BF16 ? 8 : 4) != 0)
     return NVFP4_ERR_MISALIGNED;
   const AttnWorkspace w = attn_workspace(batch->tokens, batch->n_seqs, n_heads, cache->n_kv_heads, cache->head_dim);
+  if (!w.fits()) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (workspace_bytes < w.bytes) return NVFP4_ERR_INVALID_ARG;
   DeviceInfo *dev = nullptr;
   if (nvfp4_status_t st = current_device(&dev)) return st;
@@ -1185,7 +1188,6 @@ nvfp4_status_t nvfp4_attention(const void *q_bf16, int64_t ld_q, int n_heads, co
   a.prompt_ml = reinterpret_cast<float2 *>(base + w.prompt_ml);
   a.prompt_part = reinterpret_cast<float *>(base + w.prompt_part);
   auto launch_prompt = [&](auto kernel, auto join, int tile_rows, int smem) {
-    if (w.items * a.splits > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (nvfp4_status_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(w.items * a.splits)),
                                       dim3(attn::prompt::kThreads), smem, s, 1, a, k_map))
       return e;
