@@ -183,7 +183,10 @@ __device__ __forceinline__ float log_scale(float s) {
   if ((b & 0x7fffffu) == 0) f = 0.0f;
   return b < 0x7f800000u ? float(int(b >> 23) - 127) + f : __int_as_float(0x7fffffff);
 }
-__device__ __forceinline__ float inverse_scale(float s) { return 1.0f / fmaxf(s, 0x1p-100f); }
+// 2^-18 / sV, the factor of a weight in the denominator.  A row has fewer than 2^31 tokens with weights of up
+// to 2^15 (or 2^16 per tile of 128), and sV is at least 2^-100: with the 2^-18 their sum stays below 2^128.
+constexpr float kSumUnit = 0x1p-18f;
+__device__ __forceinline__ float inverse_scale(float s) { return kSumUnit / fmaxf(s, 0x1p-100f); }
 
 // Power of two 2^e that brings a row's largest magnitude into [2^14, 2^15) when the row is
 // multiplied by 2^-e; 0 for zero and non-finite rows.
@@ -234,7 +237,7 @@ __device__ __forceinline__ Seq scan_seq(const Args &a, int s, int &high, int (&s
 template <int D>
 struct DecodeSmem {
   uint64_t full[kWarps][Cfg<D>::STAGES];
-  float4 scales[kWarps][Cfg<D>::STAGES][Cfg<D>::NG];  // (sK, log2 sV, 1 / sV, -) of each 16-token tile; sK < 0: no tokens there
+  float4 scales[kWarps][Cfg<D>::STAGES][Cfg<D>::NG];  // (sK, log2 sV, kSumUnit / sV, -) of each 16-token tile; sK < 0: no tokens there
   float m[kWarps][kRows], l[kWarps][kRows];
   int lim[kRows];
   int nan_first[D];  // first token, among those that some rows of the unit do not see, whose value is NaN
@@ -606,7 +609,7 @@ __device__ bool decode_segment(const Args &a, const CUtensorMap *k_map, const CU
       *reinterpret_cast<float2 *>(a.part + (int64_t(slot) * kRows + r) * D + c) = make_float2(o0, o1);
       if (c == 0) a.part_ml[slot * kRows + r] = make_float2(M, l);
     } else {
-      const float f = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: the row is 0
+      const float f = l == 0.0f ? 0.0f : kSumUnit / l;  // no visible token: the row is 0
       const int R = rg * kRows + r;
       const int64_t at = (sq.start + R / a.group) * a.ld_out + int64_t(h * a.group + R % a.group) * D + c;
       if (a.out_fp32)
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(Join<D>::THREADS) combine_kernel(const __grid_
     l = fmaf(sl[k][r], f, l);
     o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
   }
-  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  const float f = l == 0.0f ? 0.0f : kSumUnit / l;
   const int64_t at = (sq.start + R / a.group) * a.ld_out + int64_t(u.y * a.group + R % a.group) * D + 4 * col;
   if (a.out_fp32) {
     *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);

@@ -656,7 +656,7 @@ __device__ __forceinline__ float row_max(uint32_t s_tmem, const Scales *sc, floa
   return mt;
 }
 
-// P = 2^(x - base) over the row of S as FP16 in p, sum of P / sV in l; returns the sum of
+// P = 2^(x - base) over the row of S as FP16 in p, sum of P kSumUnit / sV in l; returns the sum of
 // P (NaN if a score is).  MASK: only the first `vis` columns.
 template <int D, bool MASK>
 __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, float rc, float base, int vis,
@@ -854,7 +854,7 @@ __device__ void softmax(const Args &a, Control<D> &c, const Item &it, int n_tile
   if (!__all_sync(0xffffffffu, mbar_wait(&c.o_done[C::kSplitKV ? (n_tiles - 1) & 1 : w], phase<D>(n_tiles - 1)))) return;
   tc_fence_after();
   const bool empty = m_ref == -INFINITY && l == l;  // no visible token (a NaN score leaves m_ref, not l)
-  const float f = 1.0f / l;
+  const float f = kSumUnit / l;
   constexpr int kCols = C::kSplitKV ? D / 2 : D;
   const int col0 = C::kSplitKV ? w * kCols : 0;
   const int64_t at = (it.sq.start + tok) * a.ld_out + int64_t(head) * D;
@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       o[n].x = fmaf(v.x, f, o[n].x), o[n].y = fmaf(v.y, f, o[n].y), o[n].z = fmaf(v.z, f, o[n].z), o[n].w = fmaf(v.w, f, o[n].w);
     }
   }
-  const float f = M == -INFINITY && l == l ? 0.0f : 1.0f / l;  // no visible token, and no NaN score: 0
+  const float f = M == -INFINITY && l == l ? 0.0f : kSumUnit / l;  // no visible token, and no NaN score: 0
   const int64_t row = (it.sq.start + R / a.group) * a.ld_out + int64_t(it.h * a.group + R % a.group) * D;
 #pragma unroll
   for (int n = 0; n < N; ++n) {

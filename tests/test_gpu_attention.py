@@ -385,3 +385,29 @@ def test_prompts_around_tile_ends(nv, d, n_tiles):
         kv = 128 * n_tiles + extra
         for causal in (True, False):
             run_case(nv, [65, 70], [kv, max(kv - 57, 70)], 2, 1, d, 16, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("growth", [0.0, 2.5, 9.0])
+def test_denominators_of_long_rows_with_the_smallest_value_scale(nv, d, q_len, growth):
+    """700000 tokens of one value at the smallest scale: the output is that value.  The scores of
+    the first tile are lower, so that the others' weights exceed the reference by 2^growth."""
+    import torch
+    block, kv = 128, 700_000
+    k = torch.zeros((2, 1, block, d), dtype=torch.uint8, device="cuda")
+    k[1, :, :, 0] = 0x38  # 1.0
+    v = torch.full_like(k, 0x3C)  # 1.5
+    one = torch.ones((2, 1), device="cuda")
+    cache = nv.BlockKVCache(k, v, one, one * 2.0 ** -100)
+    table = torch.ones((1, -(-kv // block)), dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    q = torch.zeros((q_len, d), dtype=torch.bfloat16, device="cuda")
+    q[:, 0] = growth
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    got = nv.attention(q, i32(0, q_len), i32(kv), table, cache, softmax_scale=float(np.log(2.0)), causal=False, out_dtype="f32")
+    # FP16's rounding of one weight for all, 2^-11; sums of 700000 / 16 terms in one chain at worst, each
+    # addition within 2^-23, above and below
+    bound = 2.0 ** -11 + 2 * 700_000 / 16 * 2.0 ** -23
+    want = 1.5 * 2.0 ** -100
+    assert float((got.double() / want - 1.0).abs().max()) <= bound
