@@ -494,8 +494,10 @@ NVFP4_API size_t nvfp4_attention_workspace_bytes(int64_t tokens, int64_t n_seqs,
  *   no token is 0.  What no row sees (places behind a sequence's end, later tokens) has no
  *   influence, NaN included.  FP32 maxima, sums and accumulators.  q is scaled by a power of
  *   two per row and keeps its BF16 bits: few new tokens take it as FP16, exact down to 2^-29 of the
- *   row's largest value, prompts as the sum of two E4M3 parts, exact down to 2^-10 of it and to
- *   2^-18 of it in absolute terms below.  The weights p are rounded to FP16's 11 bits.
+ *   row's largest value, prompts as the sum of two E4M3 parts, exact down to 2^-10 of it and
+ *   within 2^-17 of it below.  In the numerator a weight times its block's value scale is
+ *   rounded to FP16: to 11 bits down to 2^-26 (prompts: 2^-20) of the largest such product
+ *   of the row, and below that to within 2^-37 (2^-31) of it; the denominator keeps FP32.
  *   q: device BF16 [tokens x ld_q], head h at column h * head_dim, 16-byte aligned,
  *   ld_q % 8 == 0.  out: device, BF16 (ld_out % 8 == 0) or FP32 (ld_out % 4 == 0) per
  *   out_kind, 16-byte aligned.  Cache scales must be positive; powers of two (as

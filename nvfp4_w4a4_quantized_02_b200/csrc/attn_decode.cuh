@@ -6,14 +6,17 @@
 // running maximum; the maximum is taken over x_j + log2 sV_j, so that the weights the
 // matrix instruction sees,
 //     P_j = 2^{x_j + log2 sV_j - M + kBoost},
-// already hold the value scale and are at most 2^kBoost, while the denominator adds
-// P_j / sV_j.  kBoost keeps weights down to 2^-36 of the largest above the FP16 subnormals.
-// M need not be the maximum itself: it follows when a weight would exceed 2^(kBoost + kSlack).
+// already hold the value scale, while the denominator adds P_j / sV_j.  M need not be the maximum
+// itself: it follows when a P would exceed 2^(kBoost + kSlack), FP16's range being 2^16.  P is rounded
+// to FP16, the operand type that E4M3 values are exact in: with 11 bits down to 2^-26 of 2^kBoost,
+// FP16's smallest normal number, and below that to within half its smallest step, 2^-37 of 2^kBoost.
 //
-// Bound by HBM: every cached byte is read once per kv head, for 2 x 8 multiply-adds.  Each warp
-// keeps its own ring of STAGES steps of K and V rows in shared memory, filled by TMA, so that
-// about 190 KB are on their way to an SM whatever its warps do (loads straight into registers reached
-// 3.3 TB/s on 32 sequences of up to 8192 tokens), and feeds mma.m16n8k16 from it:
+// Bound by HBM: a unit is eight query rows of a kv head (heads of a group, times tokens) and reads
+// every cached byte of its sequence once, for 2 x 8 multiply-adds; 9 to 32 rows are two to four
+// units and read the cache as often.  Each warp keeps its own ring of STAGES steps of K and V rows in shared
+// memory, filled by TMA, so that about 190 KB (at 64 values per head half of that) are on their way to an SM
+// whatever its warps do (loads straight into registers reached 3.3 TB/s on 32 sequences of up to
+// 8192 tokens), and feeds mma.m16n8k16 from it:
 //  * S^T = K Q^T has the cached tokens as its 16 rows and up to 8 query rows (the heads of
 //    a group, times tokens) as its 8 columns.  The contraction runs over the head's
 //    values in any order as long as K and Q agree, so a lane takes 16 consecutive bytes

@@ -6,9 +6,10 @@
 //  * S = Q K^T runs on the codes themselves: K goes by TMA straight into its operand layout,
 //    and q, scaled by a power of two per row, is the sum of two E4M3 parts, hi = E4M3(q) and
 //    lo = E4M3(q - hi).  A BF16 value has 8 significant bits and each part holds 4, so the sum is exact
-//    down to 2^-10 of the row's largest value (and to 2^-18 of it in absolute terms below).  Two FP8
-//    products cost what one in FP16 would, and K needs no conversion.
-//  * O += P V runs in FP16, since P needs more than 8 bits of range and precision: converter
+//    down to 2^-10 of the row's largest value, and below within half of E4M3's smallest step, 2^-17 of it.
+//    Two FP8 products cost what one in FP16 would, and K needs no conversion.
+//  * O += P V runs in FP16, since P needs more than 8 bits of range and precision (11 bits down to 2^-20 of
+//    the row's reference, below that to within 2^-31 of it): converter
 //    warps load V codes (exact in FP16) and write panels of 64 values with 128-byte swizzle, token
 //    rows, which the product reads as an MN-major operand.
 // S accumulates in TMEM; a softmax thread reads a row of it and writes P over it as FP16, the A

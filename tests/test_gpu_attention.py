@@ -411,3 +411,81 @@ def test_denominators_of_long_rows_with_the_smallest_value_scale(nv, d, q_len, g
     bound = 2.0 ** -11 + 2 * 700_000 / 16 * 2.0 ** -23
     want = 1.5 * 2.0 ** -100
     assert float((got.double() / want - 1.0).abs().max()) <= bound
+
+
+def wide_queries(rng, rows, heads, d, outlier):
+    """Queries with one value per row `outlier` times the others."""
+    x = rng.standard_normal((rows, heads, d))
+    x[:, :, 5] = outlier * rng.choice([-1.0, 1.0], (rows, heads))
+    return x
+
+
+def narrow_keys(rng, count, block, d):
+    """Keys of two values, and next to nothing where the queries have their outlier."""
+    k = np.zeros((count, 1, block, d))
+    k[..., [8, 9]] = rng.standard_normal((count, 1, block, 2)) * 100.0
+    k = ref._encode(k)
+    k[..., 5] = rng.choice([0x00, 0x01, 0x81], (count, 1, block))
+    return k
+
+
+def wide_query_bound(q, k, ks, scale, parts):
+    """Largest error of a score.  Of prompts (`parts`) a value is exact down to 2^-10 of the row's largest, and
+    below it within half a step 2^-9 of the row scaled to (224, 448]; of few tokens down to 2^-29 of it,
+    and below within half a step 2^-24 of [2^14, 2^15)."""
+    top = np.abs(q).max(axis=2)
+    dq = top[..., None] * (2.0 ** -10 / 224 if parts else 2.0 ** -25 / 2.0 ** 14)
+    if parts:
+        dq = np.where(np.abs(q) >= 2.0 ** -10 * top[..., None], 0.0, dq)
+    reach = np.abs(e4m3_decode(k) * ks[..., None, None]).max(axis=(0, 1, 2))
+    return scale * (np.broadcast_to(dq, q.shape) * reach).sum(axis=2)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [3, 50])
+@pytest.mark.parametrize("log_outlier", [0, 4, 8, 11, 14])
+def test_queries_far_apart_within_a_row(nv, d, q_len, log_outlier):
+    import torch
+    rng = np.random.default_rng(log_outlier)
+    heads, kv, block = 2, 300, 32
+    cu, lens, table_d, table, count = batch([q_len], [kv], block, rng)
+    _, v, ks, vs = filled_cache(count, 1, block, d, rng)
+    k, scale = narrow_keys(rng, count, block, d), 0.25
+    q, q_d = bf16(wide_queries(rng, q_len, heads, d, 2.0 ** log_outlier))
+    got = nv.attention(q_d.reshape(q_len, -1), cu, lens, table_d, to_cache(nv, k, v, ks, vs), softmax_scale=scale, out_dtype="f32")
+    got = got.double().cpu().numpy().reshape(q.shape)
+    want, mags = ref.attention(q, [q_len], [kv], table, k, v, ks, vs, scale, True)
+    dx = wide_query_bound(q, k, ks, scale, q_len * heads > 32)[..., None]
+    biggest = np.abs(e4m3_decode(v) * vs[..., None, None]).max()
+    # scores off by dx either way move a weight's share by e^(2 dx)
+    bound = attention_bound(want, mags, biggest, 2.0 ** -24, kv) + np.expm1(2 * dx) * mags
+    assert not np.any(np.abs(got - want) > bound)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 50])
+@pytest.mark.parametrize("log_scale", [0, 6])
+@pytest.mark.parametrize("gap", [6, 14, 20, 26, 30])
+def test_weights_far_below_the_largest(nv, d, q_len, log_scale, gap):
+    """A block whose tokens outweigh all others by 2^gap and whose values are zero, at a larger
+    scale or not: the output is what the small weights make of the others' values."""
+    import torch
+    rng = np.random.default_rng(gap)
+    block, kv = 16, 200
+    cu, lens, table_d, table, count = batch([q_len], [kv], block, rng)
+    _, v, ks, _ = filled_cache(count, 1, block, d, rng)
+    k, ks, vs = np.zeros_like(v), np.ones_like(ks), np.ones_like(ks)
+    first = table[0, 0]
+    k[first, ..., 0], v[first], vs[first] = 0x38, 0, 2.0 ** log_scale
+    x = np.zeros((q_len, 1, d))
+    x[..., 0] = gap
+    q, q_d = bf16(x)
+    scale = float(np.float32(np.log(2.0)))
+    got = nv.attention(q_d.reshape(q_len, -1), cu, lens, table_d, to_cache(nv, k, v, ks, vs), softmax_scale=scale, causal=False,
+                       out_dtype="f32").double().cpu().numpy().reshape(q.shape)
+    want, mags = ref.attention(q, [q_len], [kv], table, k, v, ks, vs, scale, False)
+    # a weight times its value scale is within half a step 2^-24 of FP16 of 2^12 (few tokens) or 2^6 (prompts) for
+    # the largest one; the first block's 16 tokens make up the denominator at least
+    least = 2.0 ** (log_scale - (37 if q_len == 1 else 31)) * np.abs(e4m3_decode(v)).sum(axis=(0, 1, 2)) / 16
+    bound = 2.0 ** -24 * np.abs(want) + (2.0 ** -11 + 2.0 ** -13) * mags + least
+    assert not np.any(np.abs(got - want) > bound)
