@@ -42,6 +42,7 @@
 #pragma once
 
 #include "attn_decode.cuh"
+#include "gdn.cuh"
 
 namespace nvfp4 {
 namespace attn {
@@ -589,19 +590,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\t"
-      "mov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\t"
-      "mov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
 // 2^x for two values on the FMA pipe: 2^n 2^f with n = round(x), f in [-1/2, 1/2], and a
 // polynomial of degree 4 for 2^f (minimax in relative error by Remez' exchange, 2^-18.5, far
 // below the FP16 rounding that follows).  x is clamped to [-126, 127]; a NaN becomes 2^127, which
@@ -612,12 +600,12 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
   x.y = fminf(fmaxf_nan(x.y, -126.0f), 127.0f);
   const float2 t = add_f32x2(x, make_float2(kMagic, kMagic));
   const float2 n = add_f32x2(t, make_float2(-kMagic, -kMagic));
-  const float2 f = fma_f32x2(n, make_float2(-1.0f, -1.0f), x);
-  float2 p = fma_f32x2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+  const float2 f = gdn::ffma2(n, make_float2(-1.0f, -1.0f), x);
+  float2 p = gdn::ffma2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
                        make_float2(0.05591785907745361f, 0.05591785907745361f));
-  p = fma_f32x2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  p = fma_f32x2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  p = fma_f32x2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  p = gdn::ffma2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  p = gdn::ffma2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  p = gdn::ffma2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
   return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
@@ -676,7 +664,7 @@ __device__ __forceinline__ float row_exp(uint32_t s_tmem, const Scales *sc, floa
       float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int n = 0; n < 16; n += 2) {
-        float2 x = fma_f32x2(make_float2(__uint_as_float(v[16 * g + n]), __uint_as_float(v[16 * g + n + 1])),
+        float2 x = gdn::ffma2(make_float2(__uint_as_float(v[16 * g + n]), __uint_as_float(v[16 * g + n + 1])),
                              make_float2(ck, ck), make_float2(ce, ce));
         if constexpr (MASK) {
           if (32 * i + 16 * g + n >= vis) x.x = -INFINITY;

@@ -341,6 +341,7 @@ constexpr int kDecodeRows = 32;
 // Few prompt items (row blocks times kv heads) for the SMs: each is cut into as many parts as make
 // the CTAs fill whole waves best (1024 tokens on 32768 at four kv heads of 256 values: 192 items on
 // 148 SMs, 955 us uncut), while the parts' results fit kMaxPromptParts places.
+// The workspace's size is told without a device, so the rule takes a B200's count of SMs.
 constexpr int kMaxPromptParts = 640, kMaxSplits = 8, kSmsAssumed = 148;
 int prompt_splits(int64_t items, int most) {
   int best = 1;
