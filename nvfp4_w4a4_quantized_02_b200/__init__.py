@@ -518,18 +518,18 @@ def _rows(x, name: str, dtype, dev: int = -1) -> int:
     return stride[0] if shape[0] > 1 else shape[1]
 
 
-def _made(dev: int, stream, make, returned: bool = True):
-    """``make()``'s buffer for a call on ``stream``, taken from that stream's memory: what the
+def _made(dev: int, stream, make, *args, returned: bool = True, **kw):
+    """``make(...)``'s buffer for a call on ``stream``, taken from that stream's memory: what the
     current stream's allocator hands out may still be in use by kernels queued there, and
     nothing orders ``stream`` behind them.  The caller has a ``returned`` buffer on the
     current stream, which the allocator has to know of."""
     if stream is None or stream.cuda_stream == _raw_stream(dev):
-        return make()
+        return make(*args, **kw)
     import torch
     if stream.device.index != dev:
         raise ValueError("stream is on another device")
     with torch.cuda.stream(stream):
-        t = make()
+        t = make(*args, **kw)
     if returned:
         t.record_stream(torch.cuda.current_stream(dev))
     return t
@@ -562,7 +562,11 @@ def _out_buffer(like, shape, out, out_dtype: str, stream):
     else:
         raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
     if out is None:
-        return _made(like.get_device(), stream, lambda: like.new_empty(shape, dtype=dtype)), kind, shape[1], True
+        if stream is None:
+            out = like.new_empty(shape) if kind == 0 else like.new_empty(shape, dtype=dtype)
+        else:
+            out = _made(like.get_device(), stream, like.new_empty, shape, dtype=dtype)
+        return out, kind, shape[1], True
     ld = _rows(out, "out", dtype, like.get_device())
     if out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}")
@@ -606,7 +610,7 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     if device.type != "cuda":
         raise ValueError("device must be a CUDA device")
     dev = _current_device() if device.index is None else device.index
-    table = _made(dev, stream, lambda: torch.empty((max_positions, rot_dim), dtype=torch.float32, device=torch.device("cuda", dev)))
+    table = _made(dev, stream, torch.empty, (max_positions, rot_dim), dtype=torch.float32, device=torch.device("cuda", dev))
     _launch("nvfp4_rope_table", lib().nvfp4_rope_table, dev, stream, table.data_ptr(), max_positions, rot_dim, float(base))
     return table
 
@@ -641,18 +645,19 @@ def qk_norm_rope(q, k, w_q, w_k, positions=None, table=None, *, eps: float = 1e-
             raise ValueError("positions must be a contiguous int64 [tokens] tensor on q's device")
         most, rot = table.shape
         p_pos, p_table = positions.data_ptr(), table.data_ptr()
+    ld_qo, ld_ko = width_q, width_k
     if q_out is None:
-        q_out = _made(dev, stream, lambda: q.new_empty((tokens, width_q)))
-        ld_qo = width_q
+        q_out = q.new_empty((tokens, width_q)) if stream is None else _made(dev, stream, q.new_empty, (tokens, width_q))
     else:
         ld_qo = _rows(q_out, "q_out", bf16, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
     if k_out is None:
-        k_out = _made(dev, stream, lambda: q.new_empty((tokens, width_k)))
-        ld_ko = width_k
+        k_out = q.new_empty((tokens, width_k)) if stream is None else _made(dev, stream, q.new_empty, (tokens, width_k))
     else:
         ld_ko = _rows(k_out, "k_out", bf16, dev)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out / k_out must have the shape of q / k")
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
     if tokens:
         _launch("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope, dev, stream, q.data_ptr(), ld_q, k.data_ptr(),
                 ld_k, tokens, width_q // d, width_k // d, d, w_q.data_ptr(), w_k.data_ptr(), weight_offset, eps,
@@ -706,13 +711,22 @@ def attention(q, cu_seqlens, kv_lens, block_table, cache: BlockKVCache, *, softm
     L = lib()
     if workspace is None:
         need = L.nvfp4_attention_workspace_bytes(tokens, b.n_seqs, width // d, c.n_kv_heads, d)
-        workspace = _made(dev, stream, lambda: q.new_empty(max(need, 16), dtype=_U8), returned=False)
+        need = max(need, 16)
+        workspace = (q.new_empty(need, dtype=_U8) if stream is None
+                     else _made(dev, stream, q.new_empty, need, dtype=_U8, returned=False))
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous, on q's device")
     _launch("nvfp4_attention", L.nvfp4_attention, dev, stream, q.data_ptr(), ld_q, width // d, b, c,
             d ** -0.5 if softmax_scale is None else softmax_scale, causal, out.data_ptr(), kind, ld_out,
             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
+
+
+def _check_gs(g, dev: int):
+    if g.get_device() != dev:
+        raise ValueError("a global scale is on another device")
+    if g.dtype is not _F32 or g.numel() < 1:
+        raise ValueError("a global scale must be a float32 tensor of one value")
 
 
 def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: str = "bf16", out=None, stream=None):
@@ -727,26 +741,25 @@ def matvec(x, w: NVFP4Tensor, segments: Optional[Sequence] = None, out_dtype: st
         raise ValueError("x must have the weight's columns")
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError("the weight is on another device")
-    if not (codes.dtype == scales.dtype == _U8 and codes.is_contiguous() and scales.is_contiguous()
-            and codes.numel() >= rows * cols // 2 and scales.numel() >= -(-rows // 128) * 128 * (-(-cols // 64) * 4)):
+    if not (codes.dtype is scales.dtype is _U8 and codes.is_contiguous() and scales.is_contiguous()
+            and codes.numel() >= rows * cols >> 1 and scales.numel() >= (rows + 127 >> 7) * (cols + 63 >> 6) << 9):
         raise ValueError("the weight must be contiguous uint8 codes [rows, cols / 2] and scales of scale_bytes(rows, cols)")
     out, kind, ldo, made = _out_buffer(x, (x.shape[0], rows), out, out_dtype, stream)
     if not made and out.data_ptr() == x.data_ptr():
         raise ValueError("out must not be x")
-    for g in (w.gs,) if segments is None else [g for _, _, g in segments]:
-        if g.get_device() != dev:
-            raise ValueError("a global scale is on another device")
-        if g.dtype != _F32 or g.numel() < 1:
-            raise ValueError("a global scale must be a float32 tensor of one value")
-    if x.shape[0] == 0:
-        return out
     if segments is None:
-        n, segs = 1, Segment(0, rows, w.gs.data_ptr())
+        g = w.gs
+        _check_gs(g, dev)
+        n, segs = 1, Segment(0, rows, g.data_ptr())
     else:
         n = len(segments)
         if n > MAX_SEGMENTS:
             raise ValueError("too many segments")
-        segs = (Segment * n)(*[Segment(n0, n1, _ptr(g)) for n0, n1, g in segments])
+        for _, _, g in segments:
+            _check_gs(g, dev)
+        segs = (Segment * n)(*[Segment(n0, n1, g.data_ptr()) for n0, n1, g in segments])
+    if x.shape[0] == 0:
+        return out
     _launch("nvfp4_matvec", lib().nvfp4_matvec, dev, stream, x.data_ptr(), ld_x, x.shape[0],
             Operand(codes.data_ptr(), scales.data_ptr(), rows, cols), segs, n, out.data_ptr(), kind, ldo)
     return out
