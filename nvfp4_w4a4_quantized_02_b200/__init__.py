@@ -523,11 +523,11 @@ def _made(dev: int, stream, make, *args, returned: bool = True, **kw):
     current stream's allocator hands out may still be in use by kernels queued there, and
     nothing orders ``stream`` behind them.  The caller has a ``returned`` buffer on the
     current stream, which the allocator has to know of."""
+    if stream is not None and stream.device.index != dev:  # default streams have one handle on all devices
+        raise ValueError("stream is on another device")
     if stream is None or stream.cuda_stream == _raw_stream(dev):
         return make(*args, **kw)
     import torch
-    if stream.device.index != dev:
-        raise ValueError("stream is on another device")
     with torch.cuda.stream(stream):
         t = make(*args, **kw)
     if returned:
@@ -538,10 +538,11 @@ def _made(dev: int, stream, make, *args, returned: bool = True, **kw):
 def _launch(what: str, fn, dev: int, stream, *args):
     """Calls an entry point with its device current, on ``stream`` (default: the device's
     current one)."""
-    raw = _raw_stream(dev)
-    if stream is not None and stream.cuda_stream != raw:
-        if stream.device.index != dev:
-            raise ValueError("stream is on another device")
+    if stream is None:
+        raw = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError("stream is on another device")
+    else:
         raw = stream.cuda_stream
     if _current_device() == dev:
         status = fn(*args, raw)

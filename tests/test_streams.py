@@ -53,3 +53,15 @@ def test_another_stream_gives_the_memory_and_the_current_one_is_told(world):
 def test_streams_of_other_devices_are_refused(world):
     with pytest.raises(ValueError, match="another device"):
         nv._made(0, _Stream(9, device=1), world)
+
+
+def test_default_streams_of_other_devices_are_refused(world, monkeypatch):
+    """Every device's default stream has the same handle."""
+    called = []
+    for use in (lambda s: nv._made(0, s, world), lambda s: nv._launch("call", lambda *a: called.append(a) or 0, 0, s)):
+        with pytest.raises(ValueError, match="another device"):
+            use(_Stream(7, device=1))
+    monkeypatch.setattr(nv, "_current_device", lambda: 0)
+    nv._launch("call", lambda *a: called.append(a) or 0, 0, _Stream(9), 1)
+    nv._launch("call", lambda *a: called.append(a) or 0, 0, None, 2)
+    assert called == [(1, 9), (2, 7)]
