@@ -406,7 +406,8 @@ NVFP4_API nvfp4_status_t nvfp4_gdn_recurrence(const void *q_bf16, const void *k_
 /* A paged K / V cache in E4M3.  Block b of kv head h holds block_size tokens of head_dim
  * values at ((b * n_kv_heads + h) * block_size + i) * head_dim, i the token's place in the
  * block; its values mean e4m3(code) * scales[b * n_kv_heads + h].  Owned by the caller;
- * needs no initialisation.  block_size: 16, 32, 64 or 128; head_dim: 64, 128 or 256. */
+ * needs no initialisation.  Not the layout of nvfp4_kv_cache_fp8.  block_size: 16, 32, 64 or
+ * 128; head_dim: 64, 128 or 256. */
 typedef struct {
   uint8_t *k, *v;               /* device, 16-byte aligned */
   float *k_scales, *v_scales;   /* device FP32 [num_blocks][n_kv_heads] */

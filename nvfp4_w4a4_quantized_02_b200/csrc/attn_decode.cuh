@@ -38,7 +38,7 @@
 // tiles, 700 tokens, whole units took 14.9 us and cut ones 11.2 us).
 //
 // Measured, 8-bit cache: 32 sequences of up to 8192 tokens, 8 kv heads of 128 values, groups of 6:
-// 75 us, 4.5 TB/s; 2 of up to 131072, 4 kv heads of 256: 69 us, 4.4 TB/s; one of 700: 11 us, the latency of
+// 76 us, 4.5 TB/s; 2 of up to 131072, 4 kv heads of 256: 69 us, 4.4 TB/s; one of 700: 11 us, the latency of
 // two launches and a short stream.
 #pragma once
 

@@ -30,11 +30,12 @@
 // (1024) for the exponentials.  A product of 128 x 128 x 32 bytes takes 64 cycles, and a warp needs about
 // 55 to issue one with its descriptors ready (75 if it computes them).
 //
-// Measured (TFLOP/s at 4 D per visible pair).  8192 tokens, 48 + 8 heads of 128: 800 us, 1030 TFLOP/s, about
-// 3600 cycles for a tile of both streams against the tensor cores' 2048; what is left is a stream's chain
-// S -> exponentials -> P V, which one other stream does not cover.  1024 tokens on 32768, 24 + 4
-// heads of 256: 752 to 819 us, 990 to 1080 TFLOP/s; there the products with K leave the converters little of
-// shared memory (with time stamps in the kernel the MMA warp waits for V half of the time).
+// Measured (TFLOP/s at 4 D per visible pair).  8192 tokens, 48 + 8 heads of 128: 787 to 802 us, 1030 TFLOP/s
+// (call after call, at the power cap, 890 us, 930), about 3600 cycles for a tile of both streams
+// against the tensor cores' 2048; what is left is a stream's chain S -> exponentials -> P V, which one other
+// stream does not cover.  1024 tokens on 32768, 24 + 4 heads of 256: 737 to 817 us, 990 to 1100 TFLOP/s
+// (872 us, 930); there the products with K leave the converters little of shared memory (with time stamps
+// in the kernel the MMA warp waits for V half of the time).
 //
 // Warps (one CTA per SM): 0 MMA issuer, 1 producer (block table, scales, K copies), 2-3 idle, 4-7 and
 // 8-11 softmax of stream 0 and 1, 12-19 V converters.  Registers are handed from the others to the

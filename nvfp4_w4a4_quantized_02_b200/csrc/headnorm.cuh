@@ -11,7 +11,7 @@
 // shuffles instead of eight).  A warp takes a run of one token's heads and forms the products of
 // norm weight and rotation once, y = (x (w c) + x_partner (w_partner s)) / rms, which leaves three
 // packed FP32 operations per pair of values; kDepth heads' loads are in flight.  32768 tokens of 48 + 8
-// heads of 128 values, 64 rotated: 165 us, 5.7 TB/s (273 us with the rotation after the norm and one head at
+// heads of 128 values, 64 rotated: 164 us, 5.8 TB/s (273 us with the rotation after the norm and one head at
 // a time); 32 tokens: 3 us, the latency of one launch.
 #pragma once
 

@@ -11,7 +11,7 @@
 // are read and rewritten only when the scale grows.  The touched blocks are found on
 // the device: sequence s gets the slots from cu[s] / B + 2 s on, at least as many as blocks
 // that cu[s + 1] - cu[s] tokens can touch.  8 sequences of 4096 new tokens, 8 heads of 128 values: 38 us,
-// 5.3 TB/s; one new token in each of 32 sequences: 4.5 us, latency.
+// 5.3 TB/s; one new token in each of 32 sequences: 4.6 us, latency.
 #pragma once
 
 #include "batch.cuh"
